@@ -458,8 +458,8 @@ moe_status_t run_stream_gemms(const Dims& d, const Layout& L, void* ws, const Ge
 
 // The counters in the workspace start at zero (the caller zeroes a new workspace once)
 // and every kernel that uses one returns it to zero, so no call clears them.
-// first_kernel: the gate_up launch is the entry point's first kernel (no dependent
-// launch on whatever the stream ran before).
+// first_kernel: the gate_up launch is no dependent launch on whatever the stream ran before
+// (the entry point's first kernel, or one that reads the previous kernel's tables early).
 moe_status_t run_gemms(const Dims& d, const Layout& L, void* ws, const GemmJob& j,
                        cudaStream_t s, bool first_kernel, void* const* ev = nullptr) {
   if (stream_path(d)) return run_stream_gemms(d, L, ws, j, s, first_kernel, ev);
@@ -855,7 +855,10 @@ moe_status_t moe_block_forward(const moe_config_t* cfg, int32_t T, const moe_bf1
   j.w_dd = w->w_dense_down;
   j.dense_out = dense;
   j.dense_f32 = 1;
-  if ((st = run_gemms(d, L, ws, j, s, false, ev)) != MOE_OK) return st;
+  // The GEMM launch reads the routing tables before its dependency wait, which is right only
+  // if they come from a kernel that completed before the one it follows could start.  When
+  // the router also gathers, it is that one: the gate_up launch must then wait for it whole.
+  if ((st = run_gemms(d, L, ws, j, s, rgather, ev)) != MOE_OK) return st;
   if ((st = cuda_status(launch_combine_block(d.T, d.H, d.k, d.eps, x, y, inv, nullptr, topk_w,
                                              dense, w->g_post_moe,
                                              w->g_post_dense, w->g_post_ff, out, moe_out, s,
