@@ -17,7 +17,11 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = ["router.cu", "router_tc.cu", "permute.cu", "grouped_gemm.cu", "stream_gemm.cu",
-           "combine.cu", "quant.cu", "health.cu", "moe_ffn.cu"]
+           "combine.cu", "quant.cu", "health.cu", "moe_ffn.cu",
+           "act8.cu", "norm.cu", "train_gemm.cu", "train.cu"]
+HEADERS = ["common.cuh", "internal.h", "permute_impl.cuh", "warp_mma.cuh", "act8.cuh",
+           "train_internal.h"]
+INTERFACES = ["moe_ffn.h", "moe_train.h"]
 LIB = os.path.join(PKG, "libmoeffn.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -31,8 +35,8 @@ def nvcc() -> str:
 
 def build(verbose: bool = False, force: bool = False) -> str:
     srcs = [os.path.join(PKG, "csrc", s) for s in SOURCES]
-    deps = srcs + [os.path.join(PKG, "csrc", h) for h in ("common.cuh", "internal.h", "permute_impl.cuh", "warp_mma.cuh")] + [
-        os.path.join(ROOT, "include", "moe_ffn.h")]
+    deps = srcs + [os.path.join(PKG, "csrc", h) for h in HEADERS] + [
+        os.path.join(ROOT, "include", h) for h in INTERFACES]
     if not force and os.path.exists(LIB):
         t = os.path.getmtime(LIB)
         if all(os.path.getmtime(d) <= t for d in deps):

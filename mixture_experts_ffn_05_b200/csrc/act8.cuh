@@ -1,0 +1,180 @@
+// 8-bit checkpoints of activations: groups of 32 consecutive values of a row with a
+// power-of-two scale 2^k, the smallest with max|v| <= Q 2^k and k >= -126 (Q = 127 for int8
+// codes, 448 for E4M3), so that v / 2^k is exact, a code never saturates, and code * 2^k is
+// exact in bf16.  Scale byte = k + 127; 255 marks a group that held an infinity or NaN.
+// Also the loads and stores of 16- and 32-bit activations shared by the training kernels.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// Formats of an activation (the values of moe_format_t).
+constexpr int kFmtBf16 = 0, kFmtF16 = 1, kFmtF32 = 2, kFmtInt8 = 3, kFmtE4m3 = 4;
+constexpr int kGroup8 = 32;       // values that share a scale
+constexpr int kBadScale = 255;    // scale byte of a group with an infinity or NaN
+
+__host__ __device__ constexpr int fmt_bytes(int fmt) {
+  return fmt == kFmtF32 ? 4 : fmt >= kFmtInt8 ? 1 : 2;
+}
+
+// Scale byte of a group from the bits of its max|v| (the integer maximum of the absolute
+// values' bits, which orders infinities and NaN above every finite value).
+// |v|max = 1.m 2^(e-127): int8 allows 1.m <= 127/64 at k = e - 133, E4M3 1.m <= 1.75 at
+// k = e - 135, and one more otherwise.
+__device__ __forceinline__ int scale_byte(uint32_t amax_bits, bool int8) {
+  if (amax_bits >= 0x7F800000u) return kBadScale;
+  const int e = static_cast<int>(amax_bits >> 23);
+  const uint32_t m = amax_bits & 0x007FFFFFu;
+  const int k = int8 ? e - 133 + (m > 0x007E0000u) : e - 135 + (m > 0x00600000u);
+  return max(k, -126) + 127;
+}
+
+// 2^k and 2^-k of a scale byte (k + 127 in 1..248, so both are normal); NaN of a bad one.
+__device__ __forceinline__ float scale_value(int byte) {
+  return byte == kBadScale ? __uint_as_float(0x7FC00000u)
+                           : __uint_as_float(static_cast<uint32_t>(byte) << 23);
+}
+__device__ __forceinline__ float scale_inverse(int byte) {
+  return byte == kBadScale ? 0.f : __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
+}
+
+// Code of one value; inv = scale_inverse of its group (a bad group's codes are 0).
+__device__ __forceinline__ uint32_t encode1(float v, float inv, bool int8) {
+  if (inv == 0.f) return 0u;
+  const float s = v * inv;
+  if (int8) return static_cast<uint32_t>(__float2int_rn(s)) & 0xFFu;
+  return static_cast<uint32_t>(e4m3_bits_sat(s));
+}
+
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv,
+                                            bool int8) {
+  return encode1(a, inv, int8) | (encode1(b, inv, int8) << 8) | (encode1(c, inv, int8) << 16) |
+         (encode1(d, inv, int8) << 24);
+}
+
+__device__ __forceinline__ uint2 encode8(const float (&f)[8], float inv, bool int8) {
+  return make_uint2(encode4(f[0], f[1], f[2], f[3], inv, int8),
+                    encode4(f[4], f[5], f[6], f[7], inv, int8));
+}
+
+__device__ __forceinline__ float decode1(uint32_t code, float scale, bool int8) {
+  if (int8) return static_cast<float>(static_cast<int8_t>(code)) * scale;
+  const __half_raw h =
+      __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);  // exact
+  return __half2float(__half(h)) * scale;
+}
+
+__device__ __forceinline__ void decode4(uint32_t w, float scale, bool int8, float* f) {
+  if (int8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = static_cast<float>(static_cast<int8_t>(w >> (8 * i))) * scale;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+          static_cast<__nv_fp8x2_storage_t>(w >> (16 * i)), __NV_E4M3);
+      const float2 p = __half22float2(__half2(h));
+      f[2 * i] = p.x * scale;
+      f[2 * i + 1] = p.y * scale;
+    }
+  }
+}
+
+__device__ __forceinline__ void decode8(uint2 w, float scale, bool int8, float (&f)[8]) {
+  decode4(w.x, scale, int8, f);
+  decode4(w.y, scale, int8, f + 4);
+}
+
+// The integer maximum of |v| bits over the 32 lanes, and over groups of 4 lanes.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ uint32_t max4_lanes(uint32_t a) {
+  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  return max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+}
+
+// ------------------------------------------------------------ 16- and 32-bit elements
+__device__ __forceinline__ uint32_t pack2_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 pack8_f16(const float (&f)[8]) {
+  return make_uint4(pack2_f16(f[0], f[1]), pack2_f16(f[2], f[3]), pack2_f16(f[4], f[5]),
+                    pack2_f16(f[6], f[7]));
+}
+
+// Eight consecutive elements as they lie in memory (16 bytes, or 32 of fp32).
+template <int FMT>
+struct Raw8 {
+  uint4 a;
+};
+template <>
+struct Raw8<kFmtF32> {
+  uint4 a, b;
+};
+
+template <int FMT>
+__device__ __forceinline__ Raw8<FMT> load_raw8(const void* base, int64_t i) {
+  Raw8<FMT> r;
+  if constexpr (FMT == kFmtF32) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i);
+    r.a = p[0];
+    r.b = p[1];
+  } else {
+    r.a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
+  }
+  return r;
+}
+
+template <int FMT>
+__device__ __forceinline__ void widen8(const Raw8<FMT>& r, float (&f)[8]) {
+  if constexpr (FMT == kFmtF32) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+  } else if constexpr (FMT == kFmtF16) {
+    unpack8_f16(r.a, f);
+  } else {
+    unpack8(r.a, f);
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ void store8(void* base, int64_t i, const float (&f)[8]) {
+  if constexpr (FMT == kFmtF32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
+    p[0] = make_float4(f[0], f[1], f[2], f[3]);
+    p[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) =
+        FMT == kFmtF16 ? pack8_f16(f) : pack8(f);
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ float load1(const void* base, int64_t i) {
+  if constexpr (FMT == kFmtF32) return static_cast<const float*>(base)[i];
+  const uint16_t v = static_cast<const uint16_t*>(base)[i];
+  if constexpr (FMT == kFmtF16) return __half2float(*reinterpret_cast<const __half*>(&v));
+  return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+
+template <int FMT>
+__device__ __forceinline__ void store1(void* base, int64_t i, float f) {
+  if constexpr (FMT == kFmtF32) {
+    static_cast<float*>(base)[i] = f;
+  } else if constexpr (FMT == kFmtF16) {
+    static_cast<uint16_t*>(base)[i] = f16_bits(f);
+  } else {
+    static_cast<uint16_t*>(base)[i] = bf16_bits(f);
+  }
+}
+
+// The same with the format known at run time (parameters: small, read once per CTA).
+__device__ __forceinline__ float load1_any(const void* base, int64_t i, int fmt) {
+  return fmt == kFmtF32 ? load1<kFmtF32>(base, i)
+                        : fmt == kFmtF16 ? load1<kFmtF16>(base, i) : load1<kFmtBf16>(base, i);
+}
+
+}  // namespace moe

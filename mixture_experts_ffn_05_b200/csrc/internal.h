@@ -2,10 +2,16 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace moe {
+
+// The driver's tensor-map encoder (looked up once; NULL without a driver) and the current
+// device's SM count (0 on failure).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+int device_sm_count();
 
 // One GEMM problem of a grouped launch.  The weights are the M operand (rows of a
 // K-major matrix streamed by TMA), the tokens the N operand.  Output row = B row.

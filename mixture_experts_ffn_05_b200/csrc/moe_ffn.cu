@@ -284,7 +284,11 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 int g_sm_count[64] = {0};
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+}  // namespace
+
+namespace moe {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -296,7 +300,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return g_encode;
 }
 
-int sm_count() {
+int device_sm_count() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   if (g_sm_count[dev] == 0) {
@@ -307,10 +311,14 @@ int sm_count() {
   return g_sm_count[dev];
 }
 
+}  // namespace moe
+
+namespace {
+
 // K-major 2-D map: rows x cols elements, box of 128 bytes of K x box_rows rows.
 bool encode_2d(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int box_rows,
                CUtensorMapDataType dt, int elem_bytes, CUtensorMapSwizzle swz) {
-  PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem_bytes};
@@ -341,7 +349,7 @@ bool encode_i8(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int
 // memory but inside them in the box).
 bool encode_gate_up(CUtensorMap* m, const void* base, int64_t groups, int64_t F, int64_t K,
                     bool int8) {
-  PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
   if (fn == nullptr) return false;
   const int es = int8 ? 1 : 2;
   cuuint64_t dims[5] = {static_cast<cuuint64_t>(K), 8, 2, static_cast<cuuint64_t>(F / 8),
@@ -410,7 +418,7 @@ moe_status_t gather_tokens(const Dims& d, const Layout& L, void* ws, const int* 
 moe_status_t run_stream_gemms(const Dims& d, const Layout& L, void* ws, const GemmJob& j,
                               cudaStream_t s, bool first_kernel, void* const* ev) {
   const int Tk = d.T * d.k;
-  const int sms = sm_count();
+  const int sms = device_sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
   uint16_t* h = at<uint16_t>(ws, L.h);
   uint16_t* hd = at<uint16_t>(ws, L.hd);
@@ -464,7 +472,7 @@ moe_status_t run_gemms(const Dims& d, const Layout& L, void* ws, const GemmJob& 
                        cudaStream_t s, bool first_kernel, void* const* ev = nullptr) {
   if (stream_path(d)) return run_stream_gemms(d, L, ws, j, s, first_kernel, ev);
   const int64_t Tk = static_cast<int64_t>(d.T) * d.k;
-  const int grid = sm_count();
+  const int grid = device_sm_count();
   if (grid <= 0) return MOE_ERR_CUDA;
   uint16_t* h = at<uint16_t>(ws, L.h);
   uint16_t* hd = at<uint16_t>(ws, L.hd);
