@@ -277,7 +277,7 @@ moe_status_t moe_norm_forward(const moe_norm_config_t* cfg, int32_t T, const moe
 
 size_t moe_norm_workspace_size(const moe_norm_config_t* cfg, int32_t T) {
   if (check_norm(cfg, T) != MOE_OK) return 0;
-  const size_t rows = norm_backward_ctas(T, cfg->cols);
+  const size_t rows = norm_backward_max_ctas(T);
   return kAlign + align_up(rows * 2 * cfg->cols * sizeof(float));
 }
 

@@ -49,8 +49,8 @@ struct NormArgs {
   int accumulate;
   float* partials;    // backward: [CTA][d_gain | d_bias][cols]
 };
-// CTAs of the backward pass over T rows, and so rows of its partial sums.
-int norm_backward_ctas(int T, int cols);
+// The most CTAs of a backward pass over T rows, and so rows of its partial sums.
+int norm_backward_max_ctas(int T);
 cudaError_t launch_norm_forward(const NormArgs& a, int fmt, cudaStream_t s);
 cudaError_t launch_norm_backward(const NormArgs& a, int fmt, int xfmt, cudaStream_t s);
 

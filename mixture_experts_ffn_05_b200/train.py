@@ -109,15 +109,29 @@ def act8(rows: int, cols: int, fmt: str = "int8", parts: int = 1, device=None) -
                 parts)
 
 
+# The device's index of a tensor (-1: CPU) and a device's current stream as a handle: the calls
+# of one token take a few microseconds, of which torch.cuda.current_stream alone would be half.
+_get_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _Call:
     """One call's tensors: all on one device, which is current while the call is made."""
+    __slots__ = ("index", "stream")
 
     def __init__(self, first, stream):
         if isinstance(first, Act8):
             first = first.codes
         if not isinstance(first, torch.Tensor):
             raise TypeError("an activation must be a torch.Tensor or an Act8")
-        self.device, self.stream = first.device, stream
+        self.index, self.stream = first.get_device(), stream
+
+    def _on_device(self, t, name):
+        if t.get_device() != self.index or self.index < 0:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be on a CUDA device")
+            raise ValueError(f"{name} is on {t.device}, the call's first tensor on "
+                             f"{f'cuda:{self.index}' if self.index >= 0 else 'the CPU'}")
 
     def ptr(self, t, name, dtype=None, numel=None, nullable=False):
         if t is None:
@@ -128,10 +142,7 @@ class _Call:
             raise TypeError(f"{name} must be a torch.Tensor")
         if dtype is not None and t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be on a CUDA device")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the call's first tensor on {self.device}")
+        self._on_device(t, name)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         if numel is not None and t.numel() != numel:
@@ -146,7 +157,7 @@ class _Call:
                 return None
             raise ValueError(f"{name} is required")
         scales = None
-        data = t
+        width = parts * cols
         if isinstance(t, Act8):
             data = t.codes
             if data.dtype not in (torch.int8, torch.uint8):
@@ -157,28 +168,31 @@ class _Call:
                               rows * parts * (-(-cols // GROUP)))
         elif not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor or an Act8")
-        elif (t.dtype != dtype) if dtype is not None else (_FORMATS.get(t.dtype, 9) > F_F32):
-            raise TypeError(f"{name} must be {dtype or 'bf16, fp16 or fp32'}, got {t.dtype}")
-        if not data.is_cuda:
-            raise ValueError(f"{name} must be on a CUDA device")
-        if data.device != self.device:
-            raise ValueError(f"{name} is on {data.device}, the call's first tensor on {self.device}")
-        if data.dim() != 2 or data.shape[0] != rows or data.shape[1] != parts * cols:
-            raise ValueError(f"{name} must be [{rows}, {parts * cols}], got {tuple(data.shape)}")
-        ld = data.stride(0) if rows > 1 else parts * cols  # one row: its stride says nothing
-        if parts * cols > 1 and data.stride(1) != 1:
+        else:
+            data = t
+            if (t.dtype != dtype) if dtype is not None else (_FORMATS.get(t.dtype, 9) > F_F32):
+                raise TypeError(f"{name} must be {dtype or 'bf16, fp16 or fp32'}, got {t.dtype}")
+        self._on_device(data, name)
+        if data.shape != (rows, width):
+            raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(data.shape)}")
+        strides = data.stride()
+        if width > 1 and strides[1] != 1:
             raise ValueError(f"{name} must have contiguous rows")
-        return ctypes.byref(CAct(data.data_ptr(), scales, ld, _FORMATS[data.dtype]))
+        # of one row the stride says nothing
+        return CAct(data.data_ptr(), scales, strides[0] if rows > 1 else width,
+                    _FORMATS[data.dtype])
 
     def run(self, name, *args):
-        fn = getattr(_lib(), name)
-        if self.device.index == torch.cuda.current_device():
-            s = torch.cuda.current_stream() if self.stream is None else self.stream
-            _check(name, fn(*args, s.cuda_stream))
+        fn = getattr(_fns or _lib(), name)
+        index = self.index
+        s = _raw_stream(index) if self.stream is None else self.stream.cuda_stream
+        if index == _get_device():
+            st = fn(*args, s)
         else:
-            with torch.cuda.device(self.device):
-                s = torch.cuda.current_stream() if self.stream is None else self.stream
-                _check(name, fn(*args, s.cuda_stream))
+            with torch.cuda.device(index):
+                st = fn(*args, s)
+        if st:
+            _check(name, st)
 
 
 def _shape(t, name):
@@ -239,7 +253,7 @@ class NormConfig:
 
 def norm_workspace(cfg: NormConfig, T: int, device=None) -> torch.Tensor:
     """A zeroed workspace for moe_norm_backward over T rows."""
-    n = int(_lib().moe_norm_workspace_size(ctypes.byref(cfg.c()), int(T)))
+    n = int(_lib().moe_norm_workspace_size(cfg._c, int(T)))
     return _zeros(n, "moe_norm_workspace_size", device)
 
 
@@ -252,7 +266,7 @@ def moe_norm_forward(cfg, x, gain, bias, y, mean, rstd, kept: Act8 | None = None
     if kept is not None and not isinstance(kept, Act8):
         raise TypeError("kept must be an Act8")
     f32 = torch.float32
-    c.run("moe_norm_forward", ctypes.byref(cfg.c()), T, c.act(x, "x", T, cfg.cols, cfg.dtype),
+    c.run("moe_norm_forward", cfg._c, T, c.act(x, "x", T, cfg.cols, cfg.dtype),
           c.ptr(gain, "gain", cfg.param_dtype, cfg.cols, True),
           c.ptr(bias, "bias", cfg.param_dtype, cfg.cols, True),
           c.act(y, "y", T, cfg.cols, cfg.dtype), c.ptr(mean, "mean", f32, T, True),
@@ -266,7 +280,7 @@ def moe_norm_backward(cfg, x, gain, mean, rstd, dy, dx, d_gain, d_bias, ws,
     T, n = _shape(x, "x")
     c = _Call(x, stream)
     f32 = torch.float32
-    c.run("moe_norm_backward", ctypes.byref(cfg.c()), T, c.act(x, "x", T, cfg.cols, cfg.dtype),
+    c.run("moe_norm_backward", cfg._c, T, c.act(x, "x", T, cfg.cols, cfg.dtype),
           c.ptr(gain, "gain", cfg.param_dtype, cfg.cols, True),
           c.ptr(mean, "mean", f32, T, True), c.ptr(rstd, "rstd", f32, T),
           c.act(dy, "dy", T, cfg.cols, cfg.dtype), c.act(dx, "dx", T, cfg.cols, cfg.dtype),
@@ -294,7 +308,7 @@ class MlpConfig:
 
 def mlp_workspace(cfg: MlpConfig, T: int, device=None) -> torch.Tensor:
     """A zeroed workspace for moe_mlp_forward and moe_mlp_backward over T rows."""
-    n = int(_lib().moe_mlp_workspace_size(ctypes.byref(cfg.c()), int(T)))
+    n = int(_lib().moe_mlp_workspace_size(cfg._c, int(T)))
     return _zeros(n, "moe_mlp_workspace_size", device)
 
 
@@ -304,7 +318,7 @@ def moe_mlp_forward(cfg, x, w_gate_up, w_down, y, ws, kept_gu=None, stream=None)
     T, n = _shape(x, "x")
     H, D = cfg.hidden, cfg.inter
     c = _Call(x, stream)
-    c.run("moe_mlp_forward", ctypes.byref(cfg.c()), T, c.act(x, "x", T, H, cfg.dtype),
+    c.run("moe_mlp_forward", cfg._c, T, c.act(x, "x", T, H, cfg.dtype),
           c.ptr(w_gate_up, "w_gate_up", cfg.dtype, 2 * D * H),
           c.ptr(w_down, "w_down", cfg.dtype, D * H), c.act(y, "y", T, H, cfg.dtype),
           c.act(kept_gu, "kept_gu", T, D, cfg.dtype, 2, True), c.ptr(ws, "ws", torch.uint8),
@@ -322,7 +336,7 @@ def moe_mlp_backward(cfg, x, gu, w_gate_up, w_down, dy, dx, dw_gate_up, dw_down,
     grad = next((g.dtype for g in (dw_gate_up, dw_down) if g is not None), cfg.dtype)
     if grad not in (cfg.dtype, torch.float32):
         raise TypeError(f"weight gradients must be {cfg.dtype} or torch.float32, got {grad}")
-    c.run("moe_mlp_backward", ctypes.byref(cfg.c()), T,
+    c.run("moe_mlp_backward", cfg._c, T,
           c.act(x, "x", T, H, cfg.dtype, nullable=dw_gate_up is None),
           c.act(gu, "gu", T, D, cfg.dtype, 2),
           c.ptr(w_gate_up, "w_gate_up", cfg.dtype, 2 * D * H, dx is None),
