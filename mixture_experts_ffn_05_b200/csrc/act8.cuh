@@ -21,13 +21,12 @@ __host__ __device__ constexpr int fmt_bytes(int fmt) {
 // Scale byte of a group from the bits of its max|v| (the integer maximum of the absolute
 // values' bits, which orders infinities and NaN above every finite value).
 // |v|max = 1.m 2^(e-127): int8 allows 1.m <= 127/64 at k = e - 133, E4M3 1.m <= 1.75 at
-// k = e - 135, and one more otherwise.
-__device__ __forceinline__ int scale_byte(uint32_t amax_bits, bool int8) {
-  if (amax_bits >= 0x7F800000u) return kBadScale;
-  const int e = static_cast<int>(amax_bits >> 23);
-  const uint32_t m = amax_bits & 0x007FFFFFu;
-  const int k = int8 ? e - 133 + (m > 0x007E0000u) : e - 135 + (m > 0x00600000u);
-  return max(k, -126) + 127;
+// k = e - 135, and one more otherwise, which the addition below carries into e.
+template <bool INT8>
+__device__ __forceinline__ int scale_byte(uint32_t amax_bits) {
+  const int e = static_cast<int>((amax_bits + (INT8 ? 0x0001FFFFu : 0x001FFFFFu)) >> 23);
+  const int b = max(e - (INT8 ? 6 : 8), 1);
+  return amax_bits >= 0x7F800000u ? kBadScale : b;
 }
 
 // 2^k and 2^-k of a scale byte (k + 127 in 1..248, so both are normal); NaN of a bad one.
@@ -52,34 +51,40 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b, float inv) {
       __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3));
 }
 
-__device__ __forceinline__ uint32_t encode1(float v, float inv, bool int8) {
-  return inv == 0.f ? 0u : (int8 ? int8_bits(v, inv) : e4m3x2(v, 0.f, inv)) & 0xFFu;
+// INT8 is a template parameter because both forms are short: as a run-time choice they would
+// both be computed for every value.
+template <bool INT8>
+__device__ __forceinline__ uint32_t encode1(float v, float inv) {
+  return inv == 0.f ? 0u : (INT8 ? int8_bits(v, inv) : e4m3x2(v, 0.f, inv)) & 0xFFu;
 }
 
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv,
-                                            bool int8) {
+template <bool INT8>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
   const uint32_t w =
-      int8 ? __byte_perm(__byte_perm(int8_bits(a, inv), int8_bits(b, inv), 0x0040),
+      INT8 ? __byte_perm(__byte_perm(int8_bits(a, inv), int8_bits(b, inv), 0x0040),
                          __byte_perm(int8_bits(c, inv), int8_bits(d, inv), 0x0040), 0x5410)
            : e4m3x2(a, b, inv) | (e4m3x2(c, d, inv) << 16);
   return inv == 0.f ? 0u : w;
 }
 
-__device__ __forceinline__ uint2 encode8(const float (&f)[8], float inv, bool int8) {
-  return make_uint2(encode4(f[0], f[1], f[2], f[3], inv, int8),
-                    encode4(f[4], f[5], f[6], f[7], inv, int8));
+template <bool INT8>
+__device__ __forceinline__ uint2 encode8(const float (&f)[8], float inv) {
+  return make_uint2(encode4<INT8>(f[0], f[1], f[2], f[3], inv),
+                    encode4<INT8>(f[4], f[5], f[6], f[7], inv));
 }
 
-__device__ __forceinline__ float decode1(uint32_t code, float scale, bool int8) {
-  if (int8) return static_cast<float>(static_cast<int8_t>(code)) * scale;
+template <bool INT8>
+__device__ __forceinline__ float decode1(uint32_t code, float scale) {
+  if (INT8) return static_cast<float>(static_cast<int8_t>(code)) * scale;
   const __half_raw h =
       __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);  // exact
   return __half2float(__half(h)) * scale;
 }
 
 // int8: code + 128 in the low mantissa byte of 2^23, from which 2^23 + 128 is taken again.
-__device__ __forceinline__ void decode4(uint32_t w, float scale, bool int8, float* f) {
-  if (int8) {
+template <bool INT8>
+__device__ __forceinline__ void decode4(uint32_t w, float scale, float* f) {
+  if (INT8) {
     const uint32_t u = w ^ 0x80808080u;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -96,9 +101,10 @@ __device__ __forceinline__ void decode4(uint32_t w, float scale, bool int8, floa
   }
 }
 
-__device__ __forceinline__ void decode8(uint2 w, float scale, bool int8, float (&f)[8]) {
-  decode4(w.x, scale, int8, f);
-  decode4(w.y, scale, int8, f + 4);
+template <bool INT8>
+__device__ __forceinline__ void decode8(uint2 w, float scale, float (&f)[8]) {
+  decode4<INT8>(w.x, scale, f);
+  decode4<INT8>(w.y, scale, f + 4);
 }
 
 // The integer maximum of |v| bits over the 32 lanes, and over groups of 4 lanes.

@@ -2,11 +2,16 @@
 // input written or read in the same pass.
 //
 // A team of W warps holds one row, NV times 8 elements a thread, so x is read from memory once
-// although the statistics need it twice.  The teams of a CTA work on rows of their own and
-// meet at named barriers of their own.  The kernels are bound by HBM: forward reads x and
-// writes y, backward reads x (2, 4 or 1 + 1/32 bytes) and dy and writes dx.  Rows come through
-// a ring in shared memory that cp.async fills up to four rows ahead, which keeps 50 to 200 KB
-// of loads in flight per SM without registers and whatever phase the teams are in.
+// although the statistics need it twice.  The teams of a CTA (one per SM) work on rows of their
+// own and meet at named barriers of their own.  The kernels are bound by HBM: forward reads x
+// and writes y, backward reads x (2, 4 or 1 + 1/32 bytes) and dy and writes dx.  Rows come
+// through a ring in shared memory that cp.async fills up to four rows ahead, which keeps
+// 50 to 200 KB of loads in flight per SM without registers and whatever phase the teams are
+// in.  Gain and bias lie in shared memory in fp32.
+//
+// What is left to the instruction slots decides beside HBM: a row costs a warp about 9 NV + 8
+// tens of instructions (the sums over lanes and warps, the ring, the row's addresses), so NV is
+// what makes W (8 NV + 9) smallest: 2816 columns take 4 warps of 24 elements.
 //
 // Wide form (columns, strides and bases that 16-byte accesses fit): a thread owns units of 16
 // bytes of the activation's format, U = 8 or 4 columns, unit u at column U (t + 32 W u); it
@@ -24,38 +29,64 @@
 
 namespace moe {
 
-// Rows of up to 12 warps of 8 (16) elements a thread; longer ones take 32 elements a thread of
-// 16 warps, where 128 registers hold no more (the sums of the gradients spill there).
-__host__ __device__ constexpr int norm_threads(int nv) { return nv == 4 ? 512 : 384; }
-__host__ __device__ constexpr int norm_ctas_per_sm(int nv) { return nv == 1 ? 2 : 1; }
-constexpr int kNormMaxWarps = 16;
-constexpr int kNormRingBytes = 200 * 1024;  // per SM
+constexpr int kNormMaxWarps = 16;             // of a row
+constexpr int kNormSmem = 226 * 1024;         // of a CTA
+constexpr int kNormMaxStages = 4;
+constexpr int kNormRed = 2 * 768 / 32;         // floats of a round of sums: two a warp
+
+// Threads of a CTA: as many as the registers of 8 NV elements allow without spills (which, the
+// ring leaving little of L1, would go to L2).  NV = 4 only serves rows of more than 12288
+// columns, and spills in backward.
+__host__ __device__ constexpr int norm_forward_threads(int nv) {
+  return nv <= 2 ? 768 : nv == 3 ? 640 : 512;
+}
+__host__ __device__ constexpr int norm_backward_threads(int nv, bool layer) {
+  return nv == 1 ? 768 : nv == 3 && layer ? 384 : 512;
+}
 
 struct NormShape {
   int nv, warps, teams;  // 8-element pieces a thread, warps a row, rows side by side in a CTA
+  int stages;            // of the ring
+  int grid;
+  size_t smem;
 };
 
-static NormShape norm_shape(int cols, int64_t T) {
-  const int w1 = (cols + 255) / 256;  // warps of 8 elements a thread
-  NormShape s;
-  s.nv = w1 <= 12 ? 1 : w1 <= 24 ? 2 : 4;
-  s.warps = (w1 + s.nv - 1) / s.nv;
-  s.teams = norm_threads(s.nv) / 32 / s.warps;
-  const int64_t ctas = static_cast<int64_t>(kB200Sms) * norm_ctas_per_sm(s.nv);
-  const int64_t need = (T + ctas - 1) / ctas;  // few rows: spread over the SMs first
-  if (need < s.teams) s.teams = static_cast<int>(need);
-  return s;
-}
-
-// Ring bytes that a row's slot takes (16 more than the row: the narrow form's shift).
+// Shared bytes that a row of `cols` elements takes in the ring (16 more: the narrow form's
+// shift), and a parameter.
 __host__ __device__ constexpr int norm_slot(int cols, int es) {
   return (cols * es + 15) / 16 * 16 + 16;
 }
-// Ring depth in rows: at most 4, and what the SM's shared memory holds.
-__host__ __device__ constexpr int norm_stages(int nv, int bytes) {
-  const int row = norm_threads(nv) * nv * 8 * bytes * norm_ctas_per_sm(nv);
-  const int n = kNormRingBytes / row;
-  return n > 4 ? 4 : n < 1 ? 1 : n;
+__host__ __device__ constexpr int norm_param(int cols) { return (cols + 7) / 8 * 32; }
+
+// row: ring bytes of a row, params: shared bytes of gain and bias.  At most a row per SM: the
+// fewest elements a thread, which is the shortest way through it (a 2816-column row of one
+// token takes 2.6 us forward so, 7 us with 32 a thread).  Else the least instructions; fp32 has
+// half the elements per byte and takes NV <= 2, with more warps to overlap.
+template <typename Threads>
+static NormShape norm_shape(int cols, int64_t T, int es, int row, int params, Threads threads) {
+  NormShape s{};
+  int best = 0;
+  for (int nv = 1; nv <= 4; ++nv) {
+    const int w = (cols + 256 * nv - 1) / (256 * nv);
+    if (w > kNormMaxWarps || w * 32 > threads(nv)) continue;
+    if (s.nv != 0 && (T <= kB200Sms || nv == 4 || (nv == 3 && es == 4))) break;
+    const int cost = w * (8 * nv + 9);
+    if (s.nv == 0 || cost < best) {
+      best = cost;
+      s.nv = nv;
+      s.warps = w;
+    }
+  }
+  const int64_t need = (T + kB200Sms - 1) / kB200Sms;  // few rows: spread over the SMs first
+  const int most = threads(s.nv) / 32 / s.warps;
+  s.teams = static_cast<int>(need < most ? need : most);
+  // at least two rows ahead, but for rows so long that one team cannot have them
+  while (s.teams > 1 && params + 2 * s.teams * row > kNormSmem) --s.teams;
+  s.stages = (kNormSmem - params) / (s.teams * row);
+  s.stages = s.stages > kNormMaxStages ? kNormMaxStages : s.stages;
+  s.grid = static_cast<int>(T < kB200Sms ? T : kB200Sms);
+  s.smem = static_cast<size_t>(params) + static_cast<size_t>(s.stages) * s.teams * row;
+  return s;
 }
 
 // ---- asynchronous copies of 4, 8 or 16 bytes into shared memory
@@ -78,6 +109,31 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// All groups but the newest `behind` are complete.
+__device__ __forceinline__ void cp_async_wait_all_but(int behind) {
+  if (behind >= 3)
+    cp_async_wait<3>();
+  else if (behind == 2)
+    cp_async_wait<2>();
+  else if (behind == 1)
+    cp_async_wait<1>();
+  else
+    cp_async_wait<0>();
+}
+
+// A team's rows of a tensor, one after another.
+struct Rows {
+  uint8_t* p;
+  int64_t ahead;
+  __device__ __forceinline__ Rows(const void* base, int64_t row0, int64_t bytes, int64_t step)
+      : p(static_cast<uint8_t*>(const_cast<void*>(base)) + row0 * bytes), ahead(step * bytes) {}
+  __device__ __forceinline__ uint8_t* take() {
+    uint8_t* r = p;
+    p += ahead;
+    return r;
+  }
+};
+
 template <int FMT, int NV, bool WIDE>
 struct NormThread {
   static constexpr int E = 8 * NV;              // elements a thread
@@ -96,7 +152,7 @@ struct NormThread {
     wt = t >> 5;
     lane = t & 31;
     cols = n;
-    red = buf + team * w * 2;
+    red = buf + team * w * 2;  // one warp a row: unused
     turn = 0;
   }
   __device__ __forceinline__ int unit(int u) const { return U * (t + u * tpr); }
@@ -116,7 +172,7 @@ struct NormThread {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
     if (warps == 1) return;
-    float* buf = red + turn * (kNormMaxWarps * 2);
+    float* buf = red + turn * (kNormRed);
     turn ^= 1;
     if (lane == 0) {
 #pragma unroll
@@ -124,41 +180,70 @@ struct NormThread {
     }
     sync();
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.f;
-    for (int w = 0; w < warps; ++w)
+    for (int i = 0; i < N; ++i) {
+      v[i] = lane < warps ? buf[lane * N + i] : 0.f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += buf[w * N + i];
+      for (int o = kNormMaxWarps / 2; o > 0; o /= 2) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      v[i] = __shfl_sync(0xffffffffu, v[i], 0);
+    }
   }
 
-  // Gain or bias, `absent` without one.
-  __device__ __forceinline__ void param(float (&f)[E], const void* p, int fmt, float absent) const {
+  // Gain or bias as fp32 in shared memory, `absent` without one.  Wide 16-bit formats: the
+  // first four of every eight columns lie together, then the others, so that neighbouring
+  // threads' 16-byte reads are neighbours.
+  __device__ __forceinline__ static int place(int c, int cols) {
+    if constexpr (U != 8) return c;
+    return (c >> 3) * 4 + (c & 3) + (c & 4) * ((cols + 7) / 8);
+  }
+  // Team 0 fills, each thread its own columns, all loads under way at once.
+  __device__ __forceinline__ void fill(float* dst, const void* p, int fmt, float absent) const {
+    if (team != 0) return;
+    float f[E];
 #pragma unroll
-    for (int j = 0; j < E; ++j) f[j] = p != nullptr && col(j) < cols ? load1_any(p, col(j), fmt) : absent;
+    for (int j = 0; j < E; ++j)
+      f[j] = p != nullptr && col(j) < cols ? load1_any(p, col(j), fmt) : absent;
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (col(j) < cols) dst[place(col(j), cols)] = f[j];
+  }
+  __device__ __forceinline__ void param(float (&f)[U], const float* p, int u) const {
+    const int c = unit(u);
+#pragma unroll
+    for (int e = 0; e < U; ++e) f[e] = 0.f;
+    if (c >= cols) return;
+    if constexpr (U == 1) {
+      f[0] = p[c];
+    } else {
+#pragma unroll
+      for (int k = 0; k < U / 4; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(p + place(c + 4 * k, cols));
+        f[4 * k] = v.x; f[4 * k + 1] = v.y; f[4 * k + 2] = v.z; f[4 * k + 3] = v.w;
+      }
+    }
   }
 
-  __device__ __forceinline__ void store(void* base, int64_t row0, const float (&f)[E]) const {
+  __device__ __forceinline__ void store(void* row, const float (&f)[E]) const {
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       if (unit(u) >= cols) continue;
       if constexpr (!WIDE) {
-        store1<FMT>(base, row0 + unit(u), f[u]);
+        store1<FMT>(row, unit(u), f[u]);
       } else if constexpr (FMT == kFmtF32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(base) + row0 + unit(u)) =
+        *reinterpret_cast<float4*>(static_cast<float*>(row) + unit(u)) =
             make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
       } else {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = f[8 * u + e];
-        store8<FMT>(base, row0 + unit(u), v);
+        store8<FMT>(row, unit(u), v);
       }
     }
   }
 
   // ---- the ring.  XF: the format in memory, FMT or 8-bit codes.
   template <int XF>
-  __device__ __forceinline__ void request(uint8_t* slot, const void* base, int64_t row0) const {
+  __device__ __forceinline__ void request(uint8_t* slot, const uint8_t* src) const {
     constexpr int XS = fmt_bytes(XF);
-    const uint8_t* src = static_cast<const uint8_t*>(base) + row0 * XS;
     if constexpr (WIDE) {
 #pragma unroll
       for (int u = 0; u < NU; ++u)
@@ -173,11 +258,11 @@ struct NormThread {
   // The row in the slot, its columns past the end as zeros.  8-bit codes: `byte` holds the
   // scale bytes of the warp's E groups, one a lane (see scale_bytes).
   template <int XF>
-  __device__ __forceinline__ void read(float (&f)[E], const uint8_t* slot, const void* base,
-                                       int64_t row0, int byte, bool int8) const {
+  __device__ __forceinline__ void read(float (&f)[E], const uint8_t* slot, const uint8_t* src,
+                                       int byte) const {
     constexpr int XS = fmt_bytes(XF);
-    if constexpr (!WIDE)
-      slot += reinterpret_cast<uintptr_t>(static_cast<const uint8_t*>(base) + row0 * XS) & 15;
+    constexpr bool I8 = XF == kFmtInt8;
+    if constexpr (!WIDE) slot += reinterpret_cast<uintptr_t>(src) & 15;
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       const bool in = unit(u) < cols;
@@ -190,13 +275,13 @@ struct NormThread {
       const uint8_t* at = slot + unit(u) * XS;
       if constexpr (!WIDE) {
         if constexpr (XS == 1)
-          f[u] = decode1(*at, scale, int8);
+          f[u] = decode1<I8>(*at, scale);
         else
           f[u] = load1<XF>(at, 0);
       } else if constexpr (XS == 1) {
 #pragma unroll
         for (int k = 0; k < U / 4; ++k)
-          decode4(*reinterpret_cast<const uint32_t*>(at + 4 * k), scale, int8, f + U * u + 4 * k);
+          decode4<I8>(*reinterpret_cast<const uint32_t*>(at + 4 * k), scale, f + U * u + 4 * k);
       } else if constexpr (XF == kFmtF32) {
         const float4 v = *reinterpret_cast<const float4*>(at);
         f[4 * u] = v.x; f[4 * u + 1] = v.y; f[4 * u + 2] = v.z; f[4 * u + 3] = v.w;
@@ -218,8 +303,9 @@ struct NormThread {
   }
 
   // The row's 8-bit checkpoint.  Every lane takes part in the maxima.
-  __device__ __forceinline__ void keep(const float (&f)[E], uint8_t* codes, uint8_t* scales,
-                                       bool int8) const {
+  template <bool INT8>
+  __device__ __forceinline__ void keep(const float (&f)[E], uint8_t* codes,
+                                       uint8_t* scales) const {
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       const int c = unit(u);
@@ -233,17 +319,17 @@ struct NormThread {
         m = __reduce_max_sync(0xffffffffu, m);
       }
       if (c >= cols) continue;
-      const int sb = scale_byte(m, int8);
+      const int sb = scale_byte<INT8>(m);
       const float inv = scale_inverse(sb);
       if (c % kGroup8 == 0) scales[c / kGroup8] = static_cast<uint8_t>(sb);
       if constexpr (!WIDE) {
-        codes[c] = static_cast<uint8_t>(encode1(f[u], inv, int8));
+        codes[c] = static_cast<uint8_t>(encode1<INT8>(f[u], inv));
       } else {
         uint32_t w[U / 4];
 #pragma unroll
         for (int k = 0; k < U / 4; ++k) {
           const float* v = f + U * u + 4 * k;
-          w[k] = encode4(v[0], v[1], v[2], v[3], inv, int8);
+          w[k] = encode4<INT8>(v[0], v[1], v[2], v[3], inv);
         }
         if constexpr (U == 8)
           *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
@@ -256,35 +342,41 @@ struct NormThread {
 
 // ---------------------------------------------------------------- forward
 template <int FMT, int NV, bool WIDE, bool LAYER>
-__global__ void __launch_bounds__(norm_threads(NV), norm_ctas_per_sm(NV))
-    norm_forward_kernel(NormArgs a, int warps, int teams) {
+__global__ void __launch_bounds__(norm_forward_threads(NV), 1)
+    norm_forward_kernel(NormArgs a, int warps, int teams, int stages) {
   using Th = NormThread<FMT, NV, WIDE>;
-  constexpr int E = Th::E, S = norm_stages(NV, fmt_bytes(FMT));
-  __shared__ float red[2 * kNormMaxWarps * 2];
+  constexpr int E = Th::E, U = Th::U;
+  __shared__ float red[2 * kNormRed];
   extern __shared__ uint4 ring4[];
   Th th(warps, a.cols, red);
   const float inv_n = 1.f / static_cast<float>(a.cols);
   const int64_t groups = (a.cols + kGroup8 - 1) / kGroup8;
   const int slot = norm_slot(a.cols, fmt_bytes(FMT));
-  uint8_t* ring = reinterpret_cast<uint8_t*>(ring4) + th.team * S * slot;
+  float* gain = reinterpret_cast<float*>(ring4);
+  float* bias = gain + norm_param(a.cols) / 4;  // LAYER
+  uint8_t* ring = reinterpret_cast<uint8_t*>(LAYER ? bias + norm_param(a.cols) / 4 : bias) +
+                  th.team * stages * slot;
   const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
-  int64_t row = blockIdx.x + static_cast<int64_t>(gridDim.x) * th.team;
-  auto request = [&](int64_t r, int s) {
-    if (r < a.T) th.template request<FMT>(ring + s * slot, a.x, r * a.ldx);
+  const int64_t row0 = blockIdx.x + static_cast<int64_t>(gridDim.x) * th.team;
+  int rows = static_cast<int>((a.T - row0 + step - 1) / step);  // <= 0: none
+  int asked = rows;
+  const Rows px(a.x, row0, a.ldx * Th::ES, step);
+  Rows next = px, now = px, out(a.out, row0, a.ldo * Th::ES, step);
+  Rows codes(a.codes, row0, a.ld_codes, step), scales(a.code_scales, row0, groups, step);
+  int64_t row = row0;
+  auto request = [&](int s) {
+    if (asked-- > 0) th.template request<FMT>(ring + s * slot, next.take());
     cp_async_commit();
   };
-#pragma unroll
-  for (int s = 0; s < S; ++s) request(row + s * step, s);
-  float g[E], b[E];
-  if (NV < 4) {
-    th.param(g, a.gain, a.pfmt, 1.f);
-    if (LAYER) th.param(b, a.bias, a.pfmt, 0.f);
-  }
-  for (int s = 0; row < a.T; row += step) {
+  for (int s = 0; s < stages; ++s) request(s);
+  th.fill(gain, a.gain, a.pfmt, 1.f);
+  if (LAYER) th.fill(bias, a.bias, a.pfmt, 0.f);
+  __syncthreads();
+  for (int s = 0; rows > 0; --rows, row += step) {
     float x[E], mean[1] = {0.f}, var[1] = {0.f};
-    cp_async_wait<S - 1>();
+    cp_async_wait_all_but(stages - 1);
     if (!WIDE) th.sync();  // the others' chunks
-    th.template read<FMT>(x, ring + s * slot, a.x, row * a.ldx, 0, false);
+    th.template read<FMT>(x, ring + s * slot, now.take(), 0);
     if (LAYER) {
 #pragma unroll
       for (int j = 0; j < E; ++j) mean[0] += x[j];
@@ -298,105 +390,127 @@ __global__ void __launch_bounds__(norm_threads(NV), norm_ctas_per_sm(NV))
     }
     th.sum(var);
     if (!WIDE && warps == 1) th.sync();
-    request(row + S * step, s);  // every thread of the team holds its part of the row
-    if (++s == S) s = 0;
-    const float rstd = 1.f / sqrtf(fmaf(var[0], inv_n, a.eps));
+    request(s);  // every thread of the team holds its part of the row
+    if (++s == stages) s = 0;
+    const float rstd = rsqrtf(fmaf(var[0], inv_n, a.eps));  // within 2 ulp
     if (th.t == 0) {
       a.rstd[row] = rstd;
       if (LAYER) a.mean[row] = mean[0];
     }
-    if (NV == 4) {
-      th.param(g, a.gain, a.pfmt, 1.f);
-      if (LAYER) th.param(b, a.bias, a.pfmt, 0.f);
+    if (a.codes != nullptr) {
+      if (a.int8)
+        th.template keep<true>(x, codes.take(), scales.take());
+      else
+        th.template keep<false>(x, codes.take(), scales.take());
     }
-    if (a.codes != nullptr)
-      th.keep(x, a.codes + row * a.ld_codes, a.code_scales + row * groups, a.int8);
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float z = (LAYER ? x[j] - mean[0] : x[j]) * rstd;
-      x[j] = LAYER ? fmaf(z, g[j], b[j]) : z * g[j];
+    for (int u = 0; u < Th::NU; ++u) {
+      float g[U], b[U];
+      th.param(g, gain, u);
+      if (LAYER) th.param(b, bias, u);
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        float& v = x[U * u + e];
+        const float z = (LAYER ? v - mean[0] : v) * rstd;
+        v = LAYER ? fmaf(z, g[e], b[e]) : z * g[e];
+      }
     }
-    th.store(a.out, row * a.ldo, x);
+    th.store(out.take(), x);
   }
   cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------- backward
-template <int FMT, int NV, bool WIDE, bool LAYER, bool X8>
-__global__ void __launch_bounds__(norm_threads(NV), norm_ctas_per_sm(NV))
-    norm_backward_kernel(NormArgs a, int warps, int teams) {
+// XF: the format of x, FMT or an 8-bit checkpoint.
+template <int FMT, int NV, bool WIDE, bool LAYER, int XF>
+__global__ void __launch_bounds__(norm_backward_threads(NV, LAYER), 1)
+    norm_backward_kernel(NormArgs a, int warps, int teams, int stages) {
   using Th = NormThread<FMT, NV, WIDE>;
-  constexpr int XF = X8 ? kFmtInt8 : FMT;  // of x in the ring
-  constexpr int E = Th::E, S = norm_stages(NV, fmt_bytes(XF) + fmt_bytes(FMT));
-  __shared__ float red[2 * kNormMaxWarps * 2];
-  extern __shared__ uint4 ring4[];  // at the end the teams' sums [teams][cols]
+  constexpr bool X8 = fmt_bytes(XF) == 1;
+  constexpr int E = Th::E, U = Th::U;
+  __shared__ float red[2 * kNormRed];
+  extern __shared__ uint4 ring4[];  // gain, ring; at the end gain, the teams' sums [teams][cols]
   pdl_trigger();
   Th th(warps, a.cols, red);
   const float inv_n = 1.f / static_cast<float>(a.cols);
   const int64_t groups = (a.cols + kGroup8 - 1) / kGroup8;
   const int slot_x = norm_slot(a.cols, fmt_bytes(XF));
   const int slot = slot_x + norm_slot(a.cols, fmt_bytes(FMT));
-  uint8_t* ring = reinterpret_cast<uint8_t*>(ring4) + th.team * S * slot;
+  float* gain = reinterpret_cast<float*>(ring4);
+  float* teamsum = gain + norm_param(a.cols) / 4;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(teamsum) + th.team * stages * slot;
   const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
-  int64_t row = blockIdx.x + static_cast<int64_t>(gridDim.x) * th.team;
-  auto request = [&](int64_t r, int s) {
-    if (r < a.T) {
-      th.template request<XF>(ring + s * slot, a.x, r * a.ldx);
-      th.template request<FMT>(ring + s * slot + slot_x, a.dy, r * a.lddy);
+  const int64_t row0 = blockIdx.x + static_cast<int64_t>(gridDim.x) * th.team;
+  int rows = static_cast<int>((a.T - row0 + step - 1) / step);  // <= 0: none
+  int asked = rows, told = rows;
+  const Rows px(a.x, row0, a.ldx * fmt_bytes(XF), step);
+  const Rows pdy(a.dy, row0, a.lddy * Th::ES, step);
+  Rows next_x = px, now_x = px, next_dy = pdy, now_dy = pdy;
+  Rows out(a.out, row0, a.ldo * Th::ES, step), scales(a.x_scales, row0, groups, step);
+  Rows means(a.mean, row0, sizeof(float), step), rstds(a.rstd, row0, sizeof(float), step);
+  auto request = [&](int s) {
+    if (asked-- > 0) {
+      th.template request<XF>(ring + s * slot, next_x.take());
+      th.template request<FMT>(ring + s * slot + slot_x, next_dy.take());
     }
     cp_async_commit();
   };
   // the row's statistics and scale bytes, one row ahead
   float mean_n = 0.f, rstd_n = 0.f;
   int byte_n = 1;
-  auto small = [&](int64_t r) {
-    if (r >= a.T) return;
-    if (LAYER) mean_n = a.mean[r];
-    rstd_n = a.rstd[r];
-    if (X8) byte_n = th.scale_bytes(a.x_scales + r * groups);
+  auto small = [&] {
+    if (told-- <= 0) return;
+    if (LAYER) mean_n = *reinterpret_cast<const float*>(means.take());
+    rstd_n = *reinterpret_cast<const float*>(rstds.take());
+    if (X8) byte_n = th.scale_bytes(scales.take());
   };
-#pragma unroll
-  for (int s = 0; s < S; ++s) request(row + s * step, s);
-  small(row);
-  float g[E], dg[E], db[E];
-  if (NV < 4) th.param(g, a.gain, a.pfmt, 1.f);
+  for (int s = 0; s < stages; ++s) request(s);
+  small();
+  th.fill(gain, a.gain, a.pfmt, 1.f);
+  __syncthreads();
+  float dg[E], db[E];
 #pragma unroll
   for (int j = 0; j < E; ++j) dg[j] = db[j] = 0.f;
-  for (int s = 0; row < a.T; row += step) {
+  for (int s = 0; rows > 0; --rows) {
     const float mean = mean_n, rstd = rstd_n;
     const int byte = byte_n;
-    small(row + step);
+    small();
     float z[E], d[E];  // z, and dy then a = dy gain
     float sums[LAYER ? 2 : 1] = {};
-    if (NV == 4) th.param(g, a.gain, a.pfmt, 1.f);
-    cp_async_wait<S - 1>();
+    cp_async_wait_all_but(stages - 1);
     if (!WIDE) th.sync();
-    th.template read<XF>(z, ring + s * slot, a.x, row * a.ldx, byte, a.int8);
-    th.template read<FMT>(d, ring + s * slot + slot_x, a.dy, row * a.lddy, 0, false);
+    th.template read<XF>(z, ring + s * slot, now_x.take(), byte);
+    th.template read<FMT>(d, ring + s * slot + slot_x, now_dy.take(), 0);
     // sums of a z and (layer) of a, and this thread's share of the parameter gradients;
     // columns past the end have dy = 0 and add nothing
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      z[j] = (z[j] - mean) * rstd;
-      if (LAYER) db[j] += d[j];
-      dg[j] = fmaf(d[j], z[j], dg[j]);
-      d[j] *= g[j];
-      sums[0] = fmaf(d[j], z[j], sums[0]);
-      if (LAYER) sums[LAYER] += d[j];
+    for (int u = 0; u < Th::NU; ++u) {
+      float g[U];
+      th.param(g, gain, u);
+#pragma unroll
+      for (int e = 0; e < U; ++e) {
+        const int j = U * u + e;
+        z[j] = LAYER ? (z[j] - mean) * rstd : z[j] * rstd;
+        if (LAYER) db[j] += d[j];
+        dg[j] = fmaf(d[j], z[j], dg[j]);
+        d[j] *= g[e];
+        sums[0] = fmaf(d[j], z[j], sums[0]);
+        if (LAYER) sums[LAYER] += d[j];
+      }
     }
     th.sum(sums);
     if (!WIDE && warps == 1) th.sync();
-    request(row + S * step, s);
-    if (++s == S) s = 0;
+    request(s);
+    if (++s == stages) s = 0;
     const float c1 = sums[0] * inv_n, c2 = LAYER ? sums[LAYER] * inv_n : 0.f;
 #pragma unroll
-    for (int j = 0; j < E; ++j) d[j] = rstd * (d[j] - c2 - z[j] * c1);
-    th.store(a.out, row * a.ldo, d);
+    for (int j = 0; j < E; ++j)
+      d[j] = rstd * fmaf(-z[j], c1, LAYER ? d[j] - c2 : d[j]);
+    th.store(out.take(), d);
   }
   cp_async_wait<0>();
   // ---- the CTA's sums of the parameter gradients
   const bool single = gridDim.x == 1;
-  float* teamsum = reinterpret_cast<float*>(ring4);
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     float* fin = which == 0 ? a.d_gain : a.d_bias;
@@ -456,40 +570,29 @@ __global__ void __launch_bounds__(kRedCols * kRedLanes) norm_reduce_kernel(
 }
 
 // ---------------------------------------------------------------- launches
-int norm_backward_max_ctas(int T) { return T < 2 * kB200Sms ? T : 2 * kB200Sms; }
-
-// CTAs for T rows: as many as are resident at once.
-static int norm_grid(int64_t T, const NormShape& sh) {
-  const int64_t most = static_cast<int64_t>(kB200Sms) * norm_ctas_per_sm(sh.nv);
-  return static_cast<int>(T < most ? T : most);
-}
+int norm_backward_max_ctas(int T) { return T < kB200Sms ? T : kB200Sms; }
 
 template <typename K>
-static cudaError_t norm_launch(K kernel, const NormShape& sh, size_t smem, const NormArgs& a,
-                               cudaStream_t s) {
-  if (smem > 40 * 1024) {
+static cudaError_t norm_launch(K kernel, const NormShape& sh, const NormArgs& a, cudaStream_t s) {
+  if (sh.smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sh.smem));
     if (e != cudaSuccess) return e;
   }
-  return launch_k(kernel, dim3(norm_grid(a.T, sh)), dim3(32 * sh.warps * sh.teams), smem, s, false,
-                  a, sh.warps, sh.teams);
-}
-
-template <int FMT, int NV, bool WIDE, bool LAYER>
-static cudaError_t forward_nv(const NormArgs& a, const NormShape& sh, cudaStream_t s) {
-  constexpr int ES = fmt_bytes(FMT);
-  const size_t smem = static_cast<size_t>(sh.teams) * norm_stages(NV, ES) * norm_slot(a.cols, ES);
-  return norm_launch(norm_forward_kernel<FMT, NV, WIDE, LAYER>, sh, smem, a, s);
+  return launch_k(kernel, dim3(sh.grid), dim3(32 * sh.warps * sh.teams), sh.smem, s, false, a,
+                  sh.warps, sh.teams, sh.stages);
 }
 
 template <int FMT, bool WIDE, bool LAYER>
 static cudaError_t forward_shape(const NormArgs& a, cudaStream_t s) {
-  const NormShape sh = norm_shape(a.cols, a.T);
+  constexpr int ES = fmt_bytes(FMT);
+  const NormShape sh = norm_shape(a.cols, a.T, ES, norm_slot(a.cols, ES),
+                                  (LAYER ? 2 : 1) * norm_param(a.cols), norm_forward_threads);
   switch (sh.nv) {
-    case 1: return forward_nv<FMT, 1, WIDE, LAYER>(a, sh, s);
-    case 2: return forward_nv<FMT, 2, WIDE, LAYER>(a, sh, s);
-    default: return forward_nv<FMT, 4, WIDE, LAYER>(a, sh, s);
+    case 1: return norm_launch(norm_forward_kernel<FMT, 1, WIDE, LAYER>, sh, a, s);
+    case 2: return norm_launch(norm_forward_kernel<FMT, 2, WIDE, LAYER>, sh, a, s);
+    case 3: return norm_launch(norm_forward_kernel<FMT, 3, WIDE, LAYER>, sh, a, s);
+    default: return norm_launch(norm_forward_kernel<FMT, 4, WIDE, LAYER>, sh, a, s);
   }
 }
 
@@ -512,50 +615,53 @@ cudaError_t launch_norm_forward(const NormArgs& a, int fmt, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
-template <int FMT, int NV, bool WIDE, bool LAYER, bool X8>
-static cudaError_t backward_nv(const NormArgs& a, const NormShape& sh, cudaStream_t s) {
-  constexpr int ES = fmt_bytes(FMT), XS = X8 ? 1 : ES;
-  size_t smem = static_cast<size_t>(sh.teams) * norm_stages(NV, XS + ES) *
-                (norm_slot(a.cols, XS) + norm_slot(a.cols, ES));
-  const size_t sums = sh.teams > 1 ? static_cast<size_t>(sh.teams) * a.cols * sizeof(float) : 0;
-  if (sums > smem) smem = sums;
-  const cudaError_t e =
-      norm_launch(norm_backward_kernel<FMT, NV, WIDE, LAYER, X8>, sh, smem, a, s);
-  const int grid = norm_grid(a.T, sh);
-  if (e != cudaSuccess || grid == 1 || (a.d_gain == nullptr && a.d_bias == nullptr)) return e;
+template <int FMT, bool WIDE, bool LAYER, int XF>
+static cudaError_t backward_shape(const NormArgs& a, cudaStream_t s) {
+  constexpr int ES = fmt_bytes(FMT), XS = fmt_bytes(XF);
+  NormShape sh = norm_shape(a.cols, a.T, ES, norm_slot(a.cols, XS) + norm_slot(a.cols, ES),
+                            norm_param(a.cols),
+                            [](int nv) { return norm_backward_threads(nv, LAYER); });
+  if (sh.teams > 1) {  // the teams' sums at the end
+    const size_t sums = norm_param(a.cols) + static_cast<size_t>(sh.teams) * a.cols * sizeof(float);
+    if (sums > sh.smem) sh.smem = sums;
+  }
+  cudaError_t e;
+  switch (sh.nv) {
+    case 1: e = norm_launch(norm_backward_kernel<FMT, 1, WIDE, LAYER, XF>, sh, a, s); break;
+    case 2: e = norm_launch(norm_backward_kernel<FMT, 2, WIDE, LAYER, XF>, sh, a, s); break;
+    case 3: e = norm_launch(norm_backward_kernel<FMT, 3, WIDE, LAYER, XF>, sh, a, s); break;
+    default: e = norm_launch(norm_backward_kernel<FMT, 4, WIDE, LAYER, XF>, sh, a, s); break;
+  }
+  if (e != cudaSuccess || sh.grid == 1 || (a.d_gain == nullptr && a.d_bias == nullptr)) return e;
   return launch_k(norm_reduce_kernel,
                   dim3((a.cols + kRedCols - 1) / kRedCols, a.d_bias != nullptr ? 2 : 1),
-                  dim3(kRedCols * kRedLanes), 0, s, true, a.partials, grid, a.cols, a.d_gain,
+                  dim3(kRedCols * kRedLanes), 0, s, true, a.partials, sh.grid, a.cols, a.d_gain,
                   a.d_bias, a.accumulate);
 }
 
-template <int FMT, bool WIDE, bool LAYER, bool X8>
-static cudaError_t backward_shape(const NormArgs& a, cudaStream_t s) {
-  const NormShape sh = norm_shape(a.cols, a.T);
-  switch (sh.nv) {
-    case 1: return backward_nv<FMT, 1, WIDE, LAYER, X8>(a, sh, s);
-    case 2: return backward_nv<FMT, 2, WIDE, LAYER, X8>(a, sh, s);
-    default: return backward_nv<FMT, 4, WIDE, LAYER, X8>(a, sh, s);
-  }
-}
-
-template <int FMT, bool X8>
+template <int FMT, int XF>
 static cudaError_t backward_fmt(const NormArgs& a, cudaStream_t s) {
   constexpr int u = 16 / fmt_bytes(FMT);
   const bool wide = a.cols % u == 0 && a.ldx % u == 0 && a.ldo % u == 0 && a.lddy % u == 0;
   if (a.layer)
-    return wide ? backward_shape<FMT, true, true, X8>(a, s)
-                : backward_shape<FMT, false, true, X8>(a, s);
-  return wide ? backward_shape<FMT, true, false, X8>(a, s)
-              : backward_shape<FMT, false, false, X8>(a, s);
+    return wide ? backward_shape<FMT, true, true, XF>(a, s)
+                : backward_shape<FMT, false, true, XF>(a, s);
+  return wide ? backward_shape<FMT, true, false, XF>(a, s)
+              : backward_shape<FMT, false, false, XF>(a, s);
+}
+
+template <int FMT>
+static cudaError_t backward_x(const NormArgs& a, int xfmt, cudaStream_t s) {
+  if (xfmt == kFmtInt8) return backward_fmt<FMT, kFmtInt8>(a, s);
+  if (xfmt == kFmtE4m3) return backward_fmt<FMT, kFmtE4m3>(a, s);
+  return backward_fmt<FMT, FMT>(a, s);
 }
 
 cudaError_t launch_norm_backward(const NormArgs& a, int fmt, int xfmt, cudaStream_t s) {
-  const bool x8 = xfmt == kFmtInt8 || xfmt == kFmtE4m3;
   switch (fmt) {
-    case kFmtBf16: return x8 ? backward_fmt<kFmtBf16, true>(a, s) : backward_fmt<kFmtBf16, false>(a, s);
-    case kFmtF16: return x8 ? backward_fmt<kFmtF16, true>(a, s) : backward_fmt<kFmtF16, false>(a, s);
-    case kFmtF32: return x8 ? backward_fmt<kFmtF32, true>(a, s) : backward_fmt<kFmtF32, false>(a, s);
+    case kFmtBf16: return backward_x<kFmtBf16>(a, xfmt, s);
+    case kFmtF16: return backward_x<kFmtF16>(a, xfmt, s);
+    case kFmtF32: return backward_x<kFmtF32>(a, xfmt, s);
   }
   return cudaErrorInvalidValue;
 }

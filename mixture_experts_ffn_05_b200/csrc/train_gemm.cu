@@ -167,47 +167,61 @@ __device__ __forceinline__ void get8(const void* base, int64_t i, float* f, bool
 }
 
 // Kept pre-activations of 32 consecutive features of one half (gate: half 0) of a row.
+template <bool INT8>
+__device__ __forceinline__ void keep32_8(const TgParams& P, int64_t row, int d, int half, int n,
+                                         const float (&v)[32]) {
+  const int64_t at = row * P.ld_gu + static_cast<int64_t>(half) * n + d;
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) m = max(m, abs_bits(v[e]));  // past n the sums are zero
+  const int b = scale_byte<INT8>(m);
+  const float inv = scale_inverse(b);
+  const int groups = (n + kGroup8 - 1) / kGroup8;
+  P.gu_scales[row * 2 * groups + half * groups + d / kGroup8] = static_cast<uint8_t>(b);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (d + 8 * c < n)
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.gu) + at + 8 * c) =
+          make_uint2(encode4<INT8>(v[8 * c], v[8 * c + 1], v[8 * c + 2], v[8 * c + 3], inv),
+                     encode4<INT8>(v[8 * c + 4], v[8 * c + 5], v[8 * c + 6], v[8 * c + 7], inv));
+}
 __device__ __forceinline__ void keep32(const TgParams& P, int64_t row, int d, int half, int n,
                                        const float (&v)[32]) {
-  const int64_t at = row * P.ld_gu + static_cast<int64_t>(half) * n + d;
-  if (P.gu_fmt == kFmtInt8 || P.gu_fmt == kFmtE4m3) {
-    const bool int8 = P.gu_fmt == kFmtInt8;
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 32; ++e) m = max(m, abs_bits(v[e]));  // past n the sums are zero
-    const int b = scale_byte(m, int8);
-    const float inv = scale_inverse(b);
-    const int groups = (n + kGroup8 - 1) / kGroup8;
-    P.gu_scales[row * 2 * groups + half * groups + d / kGroup8] = static_cast<uint8_t>(b);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (d + 8 * c < n)
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.gu) + at + 8 * c) =
-            make_uint2(encode4(v[8 * c], v[8 * c + 1], v[8 * c + 2], v[8 * c + 3], inv, int8),
-                       encode4(v[8 * c + 4], v[8 * c + 5], v[8 * c + 6], v[8 * c + 7], inv, int8));
+  if (P.gu_fmt == kFmtInt8) {
+    keep32_8<true>(P, row, d, half, n, v);
+  } else if (P.gu_fmt == kFmtE4m3) {
+    keep32_8<false>(P, row, d, half, n, v);
   } else {
+    const int64_t at = row * P.ld_gu + static_cast<int64_t>(half) * n + d;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       if (d + 8 * c < n) put8(P.gu, at + 8 * c, v + 8 * c, P.f16);
   }
 }
 
+template <bool INT8>
+__device__ __forceinline__ void kept32_8(const TgParams& P, int64_t row, int d, int half, int n,
+                                         float (&v)[32]) {
+  const int64_t at = row * P.ld_gu + static_cast<int64_t>(half) * n + d;
+  const int groups = (n + kGroup8 - 1) / kGroup8;
+  const float s = scale_value(P.gu_scales[row * 2 * groups + half * groups + d / kGroup8]);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint2 w = make_uint2(0u, 0u);
+    if (d + 8 * c < n)
+      w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(P.gu) + at + 8 * c);
+    decode4<INT8>(w.x, s, v + 8 * c);
+    decode4<INT8>(w.y, s, v + 8 * c + 4);
+  }
+}
 __device__ __forceinline__ void kept32(const TgParams& P, int64_t row, int d, int half, int n,
                                        float (&v)[32]) {
-  const int64_t at = row * P.ld_gu + static_cast<int64_t>(half) * n + d;
-  if (P.gu_fmt == kFmtInt8 || P.gu_fmt == kFmtE4m3) {
-    const bool int8 = P.gu_fmt == kFmtInt8;
-    const int groups = (n + kGroup8 - 1) / kGroup8;
-    const float s = scale_value(P.gu_scales[row * 2 * groups + half * groups + d / kGroup8]);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint2 w = make_uint2(0u, 0u);
-      if (d + 8 * c < n)
-        w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(P.gu) + at + 8 * c);
-      decode4(w.x, s, int8, v + 8 * c);
-      decode4(w.y, s, int8, v + 8 * c + 4);
-    }
+  if (P.gu_fmt == kFmtInt8) {
+    kept32_8<true>(P, row, d, half, n, v);
+  } else if (P.gu_fmt == kFmtE4m3) {
+    kept32_8<false>(P, row, d, half, n, v);
   } else {
+    const int64_t at = row * P.ld_gu + static_cast<int64_t>(half) * n + d;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
 #pragma unroll
