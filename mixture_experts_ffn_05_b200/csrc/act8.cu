@@ -1,12 +1,14 @@
 // 8-bit activation checkpoints: write and read (see act8.cuh for the format).  Both are one
 // pass over the data and bound by HBM: bf16 moves 2 + 1 + 1/32 bytes per value each way.
 //
-// A warp takes chunks of 256 columns of a row, four at a time, so that a thread has four loads
-// under way (at 32 warps an SM 64 KB of 16-bit values, with which reads keep HBM busy).  Wide
-// form (every row starts on a 16-byte boundary and holds whole 8-element pieces): lane l owns
-// columns 8l..8l+7 of the chunk, so a group of 32 is four neighbouring lanes.  Narrow form (any
-// column count or stride): lane l owns columns l, l + 32, ..., so each access of the warp is
-// one group of 32 consecutive elements.  Groups never cross a row.
+// Wide form (every row starts on a 16-byte boundary and holds whole 8-element pieces): a group
+// of 32 columns is two neighbouring threads' two pieces each (a pair's accesses fill 32-byte
+// sectors), and the groups of all rows are dealt to the thread pairs in turn, so that short
+// rows leave no thread idle.  A thread keeps two groups' loads under way (with four 8-warp CTAs an SM 64 KB of 16-bit values, which keeps HBM busy)
+// and walks its groups by adding to pointers: at 15 instructions a value, as with a division
+// and eight values a thread, the instruction slots and not HBM were the bound.
+// Narrow form (any column count or stride): a warp takes chunks of 256 columns of a row, lane l
+// columns l, l + 32, ..., so each access of the warp is one group.
 #include "act8.cuh"
 #include "train_internal.h"
 
@@ -14,10 +16,49 @@ namespace moe {
 
 constexpr int kChunk8 = 256;
 constexpr int kActWarps = 8;
-constexpr int kActBatch = 4;   // chunks of a warp under way
+constexpr int kEncBatch = 2, kDecBatch = 4;  // groups of a thread under way
 constexpr int kActCtas = 4;    // per SM
 
-// A warp's chunks: every `stride`-th one of all rows' chunks, as row and first column.
+// A thread pair's groups: every `stride`-th one of all rows' groups.
+template <int ES>
+struct Groups {
+  uint8_t *vals, *codes, *scales;  // the next group's
+  int at, groups, at_on;           // its place in the row
+  int64_t vals_on, codes_on, stride, left;
+  int64_t vals_wrap, codes_wrap;   // added where the place passes the row's end
+  __device__ __forceinline__ Groups(const Act8Args& a) {
+    stride = static_cast<int64_t>(gridDim.x) * (kActWarps * 16);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kActWarps * 16) + (threadIdx.x >> 1);
+    const int64_t total = a.rows * a.groups;
+    left = first < total ? (total - 1 - first) / stride + 1 : 0;
+    groups = static_cast<int>(a.groups);
+    const int64_t row = first / a.groups, rows_on = stride / a.groups;
+    at = static_cast<int>(first - row * a.groups);
+    at_on = static_cast<int>(stride - rows_on * a.groups);
+    vals = static_cast<uint8_t*>(a.vals) + (row * a.ld_vals + at * kGroup8) * ES;
+    codes = a.codes + row * a.ld_codes + at * kGroup8;
+    scales = a.scales + first;
+    vals_on = (rows_on * a.ld_vals + at_on * kGroup8) * ES;
+    codes_on = rows_on * a.ld_codes + at_on * kGroup8;
+    vals_wrap = (a.ld_vals - a.groups * kGroup8) * ES;
+    codes_wrap = a.ld_codes - a.groups * kGroup8;
+  }
+  __device__ __forceinline__ void next() {
+    --left;
+    at += at_on;
+    vals += vals_on;
+    codes += codes_on;
+    scales += stride;
+    if (at >= groups) {
+      at -= groups;
+      vals += vals_wrap;
+      codes += codes_wrap;
+    }
+  }
+};
+
+// Narrow form: a warp's chunks, every `stride`-th one of all rows' chunks, as row and first
+// column.
 struct Chunks {
   int64_t left, row, at;      // chunks left; the next one's row and place in it
   int64_t rows_on, at_on, per_row;
@@ -48,36 +89,45 @@ struct Chunks {
 template <int FMT, bool WIDE, bool INT8>
 __global__ void __launch_bounds__(32 * kActWarps, kActCtas) act_encode_kernel(Act8Args a) {
   const int lane = threadIdx.x & 31;
-  Chunks ch(a);
   if constexpr (WIDE) {
-    while (ch.left > 0) {
-      Raw8<FMT> raw[kActBatch];
-      int64_t row[kActBatch], col[kActBatch];
+    constexpr int ES = fmt_bytes(FMT);
+    const int mine = 8 * (lane & 1);  // the thread's first column of a group, the other 16 on
+    Groups<ES> g(a);
+    // the warp's first thread has the most groups; the sums of a pair want the whole warp
+    for (int64_t n = __shfl_sync(0xffffffffu, g.left, 0); n > 0; n -= kEncBatch) {
+      Raw8<FMT> raw[kEncBatch][2];
+      uint8_t *codes[kEncBatch], *scales[kEncBatch];
+      int room[kEncBatch];  // columns left from the thread's first
 #pragma unroll
-      for (int b = 0; b < kActBatch; ++b) {
-        const bool in = ch.take(row[b], col[b]);
-        col[b] += 8 * lane;
-        if (!in) col[b] = a.cols;
-        raw[b] = Raw8<FMT>{};
-        if (col[b] < a.cols) raw[b] = load_raw8<FMT>(a.vals, row[b] * a.ld_vals + col[b]);
+      for (int b = 0; b < kEncBatch; ++b) {
+        room[b] = g.left > 0 ? static_cast<int>(a.cols) - g.at * kGroup8 - mine : 0;
+        codes[b] = g.codes + mine;
+        scales[b] = g.scales;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          raw[b][i] = Raw8<FMT>{};
+          if (room[b] > 16 * i) raw[b][i] = load_raw8<FMT>(g.vals + mine * ES, 16 * i);
+        }
+        g.next();
       }
 #pragma unroll
-      for (int b = 0; b < kActBatch; ++b) {
-        float f[8];
-        widen8<FMT>(raw[b], f);
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[i]));
-        const int s = scale_byte<INT8>(max4_lanes(m));
-        if (col[b] < a.cols) {
-          if ((lane & 3) == 0)
-            a.scales[row[b] * a.groups + col[b] / kGroup8] = static_cast<uint8_t>(s);
-          *reinterpret_cast<uint2*>(a.codes + row[b] * a.ld_codes + col[b]) =
-              encode8<INT8>(f, scale_inverse(s));
+      for (int b = 0; b < kEncBatch; ++b) {
+        float f[2][8];
+        widen8<FMT>(raw[b][0], f[0]);
+        widen8<FMT>(raw[b][1], f[1]);
+        uint32_t m = max(amax_bits(f[0]), amax_bits(f[1]));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        const int s = scale_byte<INT8>(m);
+        const float inv = scale_inverse(s);
+        if (room[b] > 0) {
+          if (mine == 0) *scales[b] = static_cast<uint8_t>(s);
+          *reinterpret_cast<uint2*>(codes[b]) = encode8<INT8>(f[0], inv);
         }
+        if (room[b] > 16) *reinterpret_cast<uint2*>(codes[b] + 16) = encode8<INT8>(f[1], inv);
       }
     }
   } else {
+    Chunks ch(a);
     int64_t r, c0;
     while (ch.take(r, c0)) {
       float f[8];
@@ -102,32 +152,38 @@ __global__ void __launch_bounds__(32 * kActWarps, kActCtas) act_encode_kernel(Ac
 template <int FMT, bool WIDE, bool INT8>
 __global__ void __launch_bounds__(32 * kActWarps, kActCtas) act_decode_kernel(Act8Args a) {
   const int lane = threadIdx.x & 31;
-  Chunks ch(a);
   if constexpr (WIDE) {
-    while (ch.left > 0) {
-      uint2 w[kActBatch];
-      int s[kActBatch];
-      int64_t row[kActBatch], col[kActBatch];
+    constexpr int ES = fmt_bytes(FMT);
+    const int mine = 8 * (lane & 1);  // the thread's first column of a group, the other 16 on
+    Groups<ES> g(a);
+    while (g.left > 0) {
+      uint2 w[kDecBatch][2];
+      uint8_t* vals[kDecBatch];
+      int room[kDecBatch], s[kDecBatch];
 #pragma unroll
-      for (int b = 0; b < kActBatch; ++b) {
-        const bool in = ch.take(row[b], col[b]);
-        col[b] += 8 * lane;
-        if (!in) col[b] = a.cols;
-        w[b] = make_uint2(0u, 0u);
-        s[b] = 1;
-        if (col[b] < a.cols) {
-          w[b] = *reinterpret_cast<const uint2*>(a.codes + row[b] * a.ld_codes + col[b]);
-          s[b] = a.scales[row[b] * a.groups + col[b] / kGroup8];
-        }
+      for (int b = 0; b < kDecBatch; ++b) {
+        room[b] = g.left > 0 ? static_cast<int>(a.cols) - g.at * kGroup8 - mine : 0;
+        vals[b] = g.vals + mine * ES;
+        s[b] = room[b] > 0 ? *g.scales : 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          w[b][i] = room[b] > 16 * i ? *reinterpret_cast<const uint2*>(g.codes + mine + 16 * i)
+                                    : make_uint2(0u, 0u);
+        g.next();
       }
 #pragma unroll
-      for (int b = 0; b < kActBatch; ++b) {
-        float f[8];
-        decode8<INT8>(w[b], scale_value(s[b]), f);
-        if (col[b] < a.cols) store8<FMT>(a.vals, row[b] * a.ld_vals + col[b], f);
+      for (int b = 0; b < kDecBatch; ++b) {
+        const float scale = scale_value(s[b]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float f[8];
+          decode8<INT8>(w[b][i], scale, f);
+          if (room[b] > 16 * i) store8<FMT>(vals[b], 16 * i, f);
+        }
       }
     }
   } else {
+    Chunks ch(a);
     int64_t r, c0;
     while (ch.take(r, c0)) {
       float f[8];
@@ -160,15 +216,10 @@ static cudaError_t launch_act(const Act8Args& a, bool encode, bool wide, int gri
 cudaError_t launch_act8(Act8Args a, int fmt, bool encode, cudaStream_t s) {
   const int es = fmt_bytes(fmt);
   const bool wide = a.cols % 8 == 0 && (a.rows == 1 || (a.ld_vals * es % 16 == 0 && a.ld_codes % 8 == 0));
-  if (wide && a.cols % kGroup8 == 0 && a.ld_vals == a.cols && a.ld_codes == a.cols) {
-    // rows back to back and whole groups: one long row, so that no chunk is cut short
-    a.cols *= a.rows;
-    a.groups = a.cols / kGroup8;
-    a.rows = 1;
-    a.ld_vals = a.ld_codes = a.cols;
-  }
+  if (a.rows == 1) a.ld_vals = a.ld_codes = a.cols;
   a.chunks = (a.cols + kChunk8 - 1) / kChunk8;
-  const int64_t ctas = (a.rows * a.chunks + kActWarps - 1) / kActWarps;
+  const int64_t ctas = wide ? (a.rows * a.groups + kActWarps * 16 - 1) / (kActWarps * 16)
+                            : (a.rows * a.chunks + kActWarps - 1) / kActWarps;
   const int most = kB200Sms * kActCtas;
   const int grid = static_cast<int>(ctas < most ? ctas : most);
   switch (fmt) {

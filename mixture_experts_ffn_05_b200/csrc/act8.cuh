@@ -38,17 +38,64 @@ __device__ __forceinline__ float scale_inverse(int byte) {
   return byte == kBadScale ? 0.f : __uint_as_float(static_cast<uint32_t>(254 - byte) << 23);
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void of_pair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// max(m, |a|, |b|), NaN if one is: its bits order as scale_byte wants them.
+__device__ __forceinline__ float amax3(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ uint32_t amax_bits(const float (&f)[N]) {
+  float m = fabsf(f[0]);
+  if constexpr (N % 2 == 0) m = amax3(m, f[1], f[1]);
+#pragma unroll
+  for (int i = N % 2 == 0 ? 2 : 1; i + 1 < N; i += 2) m = amax3(m, f[i], f[i + 1]);
+  return __float_as_uint(m);
+}
+
 // Codes; inv = scale_inverse of the group (0 for a bad group, whose codes are set to 0 a word
 // at a time, whatever its values gave).
 // int8: adding 1.5 2^23 rounds a value of at most 127 to an integer (nearest even) and leaves
-// its two's complement code in the low byte: one addition, where the conversion instruction
-// runs at a quarter of the rate.
+// its two's complement code in the low byte; the product with a power of two being exact, one
+// fma does both, where the conversion instruction runs at a quarter of the rate.
+constexpr float kRound8 = 12582912.f;
 __device__ __forceinline__ uint32_t int8_bits(float v, float inv) {
-  return __float_as_uint(__fadd_rn(__fmul_rn(v, inv), 12582912.f));
+  return __float_as_uint(fmaf(v, inv, kRound8));
+}
+__device__ __forceinline__ uint32_t int8x2(float a, float b, float inv) {  // in the low bytes
+  float x, y;
+  of_pair(fma2(pair_of(a, b), pair_of(inv, inv), pair_of(kRound8, kRound8)), x, y);
+  return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x0040);
 }
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b, float inv) {
-  return static_cast<uint32_t>(
-      __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3));
+  float2 p;
+  of_pair(mul2(pair_of(a, b), pair_of(inv, inv)), p.x, p.y);
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3));
 }
 
 // INT8 is a template parameter because both forms are short: as a run-time choice they would
@@ -60,10 +107,8 @@ __device__ __forceinline__ uint32_t encode1(float v, float inv) {
 
 template <bool INT8>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
-  const uint32_t w =
-      INT8 ? __byte_perm(__byte_perm(int8_bits(a, inv), int8_bits(b, inv), 0x0040),
-                         __byte_perm(int8_bits(c, inv), int8_bits(d, inv), 0x0040), 0x5410)
-           : e4m3x2(a, b, inv) | (e4m3x2(c, d, inv) << 16);
+  const uint32_t w = INT8 ? __byte_perm(int8x2(a, b, inv), int8x2(c, d, inv), 0x5410)
+                          : __byte_perm(e4m3x2(a, b, inv), e4m3x2(c, d, inv), 0x5410);
   return inv == 0.f ? 0u : w;
 }
 
@@ -81,22 +126,23 @@ __device__ __forceinline__ float decode1(uint32_t code, float scale) {
   return __half2float(__half(h)) * scale;
 }
 
-// int8: code + 128 in the low mantissa byte of 2^23, from which 2^23 + 128 is taken again.
+// int8: code + 128 in the low mantissa byte of 2^23, from which 2^23 + 128 is taken again (in
+// an operation of its own: 2^23 times the scale may overflow).
 template <bool INT8>
 __device__ __forceinline__ void decode4(uint32_t w, float scale, float* f) {
-  if (INT8) {
-    const uint32_t u = w ^ 0x80808080u;
+  const uint32_t u = w ^ 0x80808080u;
+  const uint64_t s2 = pair_of(scale, scale);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      f[i] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + i)) - 8388736.f) * scale;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 4; i += 2) {
+    if (INT8) {
+      const uint64_t p = pair_of(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + i)),
+                                 __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441 + i)));
+      of_pair(mul2(add2(p, pair_of(-8388736.f, -8388736.f)), s2), f[i], f[i + 1]);
+    } else {
       const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-          static_cast<__nv_fp8x2_storage_t>(w >> (16 * i)), __NV_E4M3);
+          static_cast<__nv_fp8x2_storage_t>(w >> (8 * i)), __NV_E4M3);
       const float2 p = __half22float2(__half2(h));
-      f[2 * i] = p.x * scale;
-      f[2 * i + 1] = p.y * scale;
+      of_pair(mul2(pair_of(p.x, p.y), s2), f[i], f[i + 1]);
     }
   }
 }
@@ -107,12 +153,7 @@ __device__ __forceinline__ void decode8(uint2 w, float scale, float (&f)[8]) {
   decode4<INT8>(w.y, scale, f + 4);
 }
 
-// The integer maximum of |v| bits over the 32 lanes, and over groups of 4 lanes.
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-__device__ __forceinline__ uint32_t max4_lanes(uint32_t a) {
-  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  return max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-}
 
 // ------------------------------------------------------------ 16- and 32-bit elements
 __device__ __forceinline__ uint32_t pack2_f16(float a, float b) {

@@ -309,9 +309,10 @@ struct NormThread {
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       const int c = unit(u);
-      uint32_t m = 0;
+      float own[U];
 #pragma unroll
-      for (int e = 0; e < U; ++e) m = max(m, abs_bits(f[U * u + e]));
+      for (int e = 0; e < U; ++e) own[e] = f[U * u + e];
+      uint32_t m = amax_bits(own);
       if constexpr (WIDE) {
 #pragma unroll
         for (int o = 1; o < 32 / U; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));

@@ -171,10 +171,7 @@ template <bool INT8>
 __device__ __forceinline__ void keep32_8(const TgParams& P, int64_t row, int d, int half, int n,
                                          const float (&v)[32]) {
   const int64_t at = row * P.ld_gu + static_cast<int64_t>(half) * n + d;
-  uint32_t m = 0;
-#pragma unroll
-  for (int e = 0; e < 32; ++e) m = max(m, abs_bits(v[e]));  // past n the sums are zero
-  const int b = scale_byte<INT8>(m);
+  const int b = scale_byte<INT8>(amax_bits(v));  // past n the sums are zero
   const float inv = scale_inverse(b);
   const int groups = (n + kGroup8 - 1) / kGroup8;
   P.gu_scales[row * 2 * groups + half * groups + d / kGroup8] = static_cast<uint8_t>(b);
