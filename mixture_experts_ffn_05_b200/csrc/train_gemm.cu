@@ -24,6 +24,7 @@ namespace moe {
 
 constexpr int kTgThreads = 320;  // producer, MMA, 8 epilogue warps
 constexpr int kTgEpiWarps = 8;
+constexpr int kTgWarpStage = 4096;  // bytes in which an epilogue warp turns its chunk around
 
 template <bool PAIR, int BN>
 struct TgCfg {
@@ -35,7 +36,7 @@ struct TgCfg {
   static constexpr int kTileM = PAIR ? 256 : 128;      // rows of an item (both CTAs of a pair)
   static constexpr int kAccCols = PAIR ? 256 : BN;     // columns of an accumulator
   static constexpr int kTmemCols = 2 * kAccCols;
-  static constexpr int kSmem = 1024 + kStages * kStage + 256;
+  static constexpr int kSmem = 1024 + kStages * kStage + kTgEpiWarps * kTgWarpStage + 256;
 };
 
 // Shared-memory descriptor of an MN-major tile laid out by TMA boxes of 64 (M or N) elements x
@@ -103,23 +104,37 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
 // ---------------------------------------------------------------- the activation
 // Both are a = g L(z) with the logistic L(z) = 1 / (1 + exp(-z)): z = g (silu) or
 // 2 sqrt(2/pi) (g + 0.044715 g^3) (gelu_tanh, since (1 + tanh w) / 2 = L(2w)).  Then
-// a' = L + g L (1 - L) z'.  For gelu_tanh z' is taken at |g| <= 16: beyond, L (1 - L) is 0 in
-// fp32 and an unbounded z' would turn it into NaN.
-struct Gate {
-  float a, da;
+// a' = L + g L (1 - L) z'.  For gelu_tanh z' is taken at g^2 <= 256: beyond, L (1 - L) is 0 in
+// fp32 and an unbounded z' would turn it into NaN.  Two values at a time.
+__device__ __forceinline__ uint64_t both(float v) { return pair_of(v, v); }
+struct Gate2 {
+  uint64_t a, da;
 };
 template <bool WITH_D>
-__device__ __forceinline__ Gate gate_of(float g, bool silu) {
-  const float c0 = 1.5957691216057308f, c1 = 0.044715f;  // 2 sqrt(2/pi)
-  const float z = silu ? g : c0 * fmaf(c1 * g, g * g, g);
-  const float l = __fdividef(1.0f, 1.0f + __expf(-z));
-  Gate r;
-  r.a = g * l;
-  r.da = 0.f;
+__device__ __forceinline__ Gate2 gate_of(uint64_t g, bool silu) {
+  constexpr float kLog2e = 1.4426950408889634f, kC0 = 1.5957691216057308f, kC1 = 0.044715f;
+  const uint64_t g2 = mul2(g, g);
+  uint64_t w = mul2(g, both(silu ? -kLog2e : -kC0 * kLog2e));  // exp(-z) = 2^w
+  if (!silu) w = mul2(w, fma2(g2, both(kC1), both(1.f)));
+  float w0, w1, l0, l1;
+  of_pair(w, w0, w1);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w0) : "f"(w0));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w1) : "f"(w1));
+  of_pair(add2(pair_of(w0, w1), both(1.f)), w0, w1);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(l0) : "f"(w0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(l1) : "f"(w1));
+  const uint64_t l = pair_of(l0, l1);
+  Gate2 r;
+  r.a = mul2(g, l);
+  r.da = 0;
   if (WITH_D) {
-    const float gc = fminf(fmaxf(g, -16.f), 16.f);
-    const float dz = silu ? 1.f : c0 * fmaf(3.f * c1 * gc, gc, 1.f);
-    r.da = fmaf(r.a * (1.f - l), dz, l);
+    uint64_t t = mul2(r.a, fma2(l, both(-1.f), both(1.f)));
+    if (!silu) {
+      float q0, q1;
+      of_pair(g2, q0, q1);
+      t = mul2(t, fma2(pair_of(fminf(q0, 256.f), fminf(q1, 256.f)), both(3.f * kC1 * kC0), both(kC0)));
+    }
+    r.da = add2(t, l);
   }
   return r;
 }
@@ -148,83 +163,210 @@ __device__ __forceinline__ TgTile tg_tile(int t, const TgParams& P) {
   return r;
 }
 
-// Stores 8 values as 16 bits.
-__device__ __forceinline__ void put8(void* base, int64_t i, const float* f, bool f16) {
-  float v[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = f[e];
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) = f16 ? pack8_f16(v) : pack8(v);
+// ---------------------------------------------------------------- an epilogue warp's chunk
+// A warp holds 32 rows x 32 columns of an accumulator, one row a lane.  Global memory is read
+// and written through a stage of the warp's own in shared memory, so that neighbouring lanes
+// touch neighbouring bytes: 8 rows of 64 bytes an instruction for 16-bit values.  (With each
+// lane on its own row an instruction touched 32 lines by half a sector, and the epilogue of
+// the dh product took 54 K cycles a tile against 32 K of the tile's MMAs.)
+// 16-byte pieces of a row are exchanged by a few bits of the row so that both sides are free
+// of bank conflicts.
+__device__ __forceinline__ int stage16(int row, int piece) { return row * 4 + (piece ^ ((row >> 1) & 3)); }
+__device__ __forceinline__ int stage32(int row, int piece) { return row * 8 + (piece ^ (row & 7)); }
+
+struct Chunk {
+  int lane, row0, m, col, n;  // first row, rows of the output; first column, columns
+  // the place of access k (of 4) in a chunk of four pieces a row
+  __device__ __forceinline__ int row(int k) const { return 8 * k + (lane >> 2); }
+  __device__ __forceinline__ int piece() const { return lane & 3; }
+  __device__ __forceinline__ bool in(int k) const {
+    return row0 + row(k) < m && col + 8 * piece() < n;
+  }
+};
+
+__device__ __forceinline__ uint4 pack16(const float* v, bool f16) {
+  return f16 ? make_uint4(pack2_f16(v[0], v[1]), pack2_f16(v[2], v[3]), pack2_f16(v[4], v[5]),
+                          pack2_f16(v[6], v[7]))
+             : make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
-__device__ __forceinline__ void get8(const void* base, int64_t i, float* f, bool f16) {
-  float v[8];
-  const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + i);
+__device__ __forceinline__ void unpack16(const uint4& u, float* v, bool f16) {
+  float t[8];
   if (f16)
-    unpack8_f16(u, v);
+    unpack8_f16(u, t);
   else
-    unpack8(u, v);
+    unpack8(u, t);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = v[e];
+  for (int e = 0; e < 8; ++e) v[e] = t[e];
 }
 
-// Kept pre-activations of 32 consecutive features of one half (gate: half 0) of a row.
+// base: the output's column 0; ld elements.
+__device__ __forceinline__ void put16(uint4* stage, const Chunk& c, void* base, int64_t ld,
+                                      const float (&v)[32], bool f16) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) stage[stage16(c.lane, i)] = pack16(v + 8 * i, f16);
+  __syncwarp();
+  uint16_t* out = static_cast<uint16_t*>(base) + static_cast<int64_t>(c.row0) * ld + c.col;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (c.in(k))
+      *reinterpret_cast<uint4*>(out + c.row(k) * ld + 8 * c.piece()) =
+          stage[stage16(c.row(k), c.piece())];
+  __syncwarp();
+}
+
+// fp32 outputs, and sums to 16- or 32-bit ones (rounded once).
+__device__ __forceinline__ void put32(uint4* stage, const Chunk& c, void* base, int64_t ld,
+                                      const float (&v)[32], bool f32, bool add, bool f16) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<float4*>(stage + stage32(c.lane, i)) =
+        make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  __syncwarp();
+  const int piece = c.lane & 7;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int r = 4 * k + (c.lane >> 3);
+    if (c.row0 + r >= c.m || c.col + 4 * piece >= c.n) continue;
+    float4 w = *reinterpret_cast<const float4*>(stage + stage32(r, piece));
+    const int64_t at = static_cast<int64_t>(c.row0 + r) * ld + c.col + 4 * piece;
+    if (f32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+      if (add) {
+        const float4 old = *o;
+        w.x += old.x; w.y += old.y; w.z += old.z; w.w += old.w;
+      }
+      *o = w;
+    } else {
+      uint2* o = reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at);
+      const uint2 old = *o;
+      float t[8];
+      unpack16(make_uint4(old.x, old.y, 0u, 0u), t, f16);
+      w.x += t[0]; w.y += t[1]; w.z += t[2]; w.w += t[3];
+      *o = f16 ? make_uint2(pack2_f16(w.x, w.y), pack2_f16(w.z, w.w))
+               : make_uint2(pack2(w.x, w.y), pack2(w.z, w.w));
+    }
+  }
+  __syncwarp();
+}
+
+// Kept pre-activations of one half (gate: 0, up: 1): columns col.. of n.
 template <bool INT8>
-__device__ __forceinline__ void keep32_8(const TgParams& P, int64_t row, int d, int half, int n,
-                                         const float (&v)[32]) {
-  const int64_t at = row * P.ld_gu + static_cast<int64_t>(half) * n + d;
+__device__ __forceinline__ void keep8(const TgParams& P, uint4* stage4, const Chunk& c, int half,
+                                      const float (&v)[32]) {
+  uint2* stage = reinterpret_cast<uint2*>(stage4);
   const int b = scale_byte<INT8>(amax_bits(v));  // past n the sums are zero
   const float inv = scale_inverse(b);
-  const int groups = (n + kGroup8 - 1) / kGroup8;
-  P.gu_scales[row * 2 * groups + half * groups + d / kGroup8] = static_cast<uint8_t>(b);
+  const int groups = (c.n + kGroup8 - 1) / kGroup8;
+  if (c.row0 + c.lane < c.m)
+    P.gu_scales[(static_cast<int64_t>(c.row0 + c.lane) * 2 + half) * groups + c.col / kGroup8] =
+        static_cast<uint8_t>(b);
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    if (d + 8 * c < n)
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.gu) + at + 8 * c) =
-          make_uint2(encode4<INT8>(v[8 * c], v[8 * c + 1], v[8 * c + 2], v[8 * c + 3], inv),
-                     encode4<INT8>(v[8 * c + 4], v[8 * c + 5], v[8 * c + 6], v[8 * c + 7], inv));
+  for (int i = 0; i < 4; ++i) {
+    const float* f = v + 8 * i;
+    stage[stage16(c.lane, i)] = make_uint2(encode4<INT8>(f[0], f[1], f[2], f[3], inv),
+                                           encode4<INT8>(f[4], f[5], f[6], f[7], inv));
+  }
+  __syncwarp();
+  uint8_t* out = static_cast<uint8_t*>(P.gu) + static_cast<int64_t>(c.row0) * P.ld_gu +
+                 static_cast<int64_t>(half) * c.n + c.col;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (c.in(k))
+      *reinterpret_cast<uint2*>(out + c.row(k) * P.ld_gu + 8 * c.piece()) =
+          stage[stage16(c.row(k), c.piece())];
+  __syncwarp();
 }
-__device__ __forceinline__ void keep32(const TgParams& P, int64_t row, int d, int half, int n,
-                                       const float (&v)[32]) {
-  if (P.gu_fmt == kFmtInt8) {
-    keep32_8<true>(P, row, d, half, n, v);
-  } else if (P.gu_fmt == kFmtE4m3) {
-    keep32_8<false>(P, row, d, half, n, v);
-  } else {
-    const int64_t at = row * P.ld_gu + static_cast<int64_t>(half) * n + d;
+__device__ __forceinline__ void keep(const TgParams& P, uint4* stage, const Chunk& c, int half,
+                                     const float (&v)[32]) {
+  if (P.gu_fmt == kFmtInt8)
+    keep8<true>(P, stage, c, half, v);
+  else if (P.gu_fmt == kFmtE4m3)
+    keep8<false>(P, stage, c, half, v);
+  else
+    put16(stage, c, static_cast<uint16_t*>(P.gu) + static_cast<int64_t>(half) * c.n, P.ld_gu, v,
+          P.f16);
+}
+
+// The same read back: requested (early, into registers) and turned into rows.
+struct Kept {
+  uint4 p[4];  // 8-bit formats: the low halves
+  int scale;
+};
+__device__ __forceinline__ Kept request_kept(const TgParams& P, const Chunk& c, int half) {
+  Kept r;
+  const int64_t at = static_cast<int64_t>(c.row0) * P.ld_gu + static_cast<int64_t>(half) * c.n +
+                     c.col + 8 * c.piece();
+  const bool eight = fmt_bytes(P.gu_fmt) == 1;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (d + 8 * c < n) put8(P.gu, at + 8 * c, v + 8 * c, P.f16);
+  for (int k = 0; k < 4; ++k) {
+    r.p[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (!c.in(k)) continue;
+    if (eight) {
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(P.gu) + at +
+                                                      c.row(k) * P.ld_gu);
+      r.p[k].x = w.x;
+      r.p[k].y = w.y;
+    } else {
+      r.p[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.gu) + at +
+                                               c.row(k) * P.ld_gu);
+    }
+  }
+  r.scale = 1;
+  if (eight && c.row0 + c.lane < c.m) {
+    const int groups = (c.n + kGroup8 - 1) / kGroup8;
+    r.scale = P.gu_scales[(static_cast<int64_t>(c.row0 + c.lane) * 2 + half) * groups +
+                          c.col / kGroup8];
+  }
+  return r;
+}
+__device__ __forceinline__ void read_kept(const TgParams& P, uint4* stage, const Chunk& c,
+                                          const Kept& r, float (&v)[32]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) stage[stage16(c.row(k), c.piece())] = r.p[k];
+  __syncwarp();
+  uint4 w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = stage[stage16(c.lane, i)];
+  __syncwarp();
+  if (fmt_bytes(P.gu_fmt) != 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack16(w[i], v + 8 * i, P.f16);
+    return;
+  }
+  const float s = scale_value(r.scale);
+  if (P.gu_fmt == kFmtInt8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      decode4<true>(w[i].x, s, v + 8 * i);
+      decode4<true>(w[i].y, s, v + 8 * i + 4);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      decode4<false>(w[i].x, s, v + 8 * i);
+      decode4<false>(w[i].y, s, v + 8 * i + 4);
+    }
   }
 }
 
-template <bool INT8>
-__device__ __forceinline__ void kept32_8(const TgParams& P, int64_t row, int d, int half, int n,
-                                         float (&v)[32]) {
-  const int64_t at = row * P.ld_gu + static_cast<int64_t>(half) * n + d;
-  const int groups = (n + kGroup8 - 1) / kGroup8;
-  const float s = scale_value(P.gu_scales[row * 2 * groups + half * groups + d / kGroup8]);
+// h = act(g) u, over g.
+__device__ __forceinline__ void glu_forward(float (&g)[32], const float (&u)[32], bool silu) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint2 w = make_uint2(0u, 0u);
-    if (d + 8 * c < n)
-      w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(P.gu) + at + 8 * c);
-    decode4<INT8>(w.x, s, v + 8 * c);
-    decode4<INT8>(w.y, s, v + 8 * c + 4);
+  for (int e = 0; e < 32; e += 2) {
+    const Gate2 ga = gate_of<false>(pair_of(g[e], g[e + 1]), silu);
+    of_pair(mul2(ga.a, pair_of(u[e], u[e + 1])), g[e], g[e + 1]);
   }
 }
-__device__ __forceinline__ void kept32(const TgParams& P, int64_t row, int d, int half, int n,
-                                       float (&v)[32]) {
-  if (P.gu_fmt == kFmtInt8) {
-    kept32_8<true>(P, row, d, half, n, v);
-  } else if (P.gu_fmt == kFmtE4m3) {
-    kept32_8<false>(P, row, d, half, n, v);
-  } else {
-    const int64_t at = row * P.ld_gu + static_cast<int64_t>(half) * n + d;
+// dg, du and h over g, u and dh.
+__device__ __forceinline__ void glu_backward(float (&dh)[32], float (&g)[32], float (&u)[32],
+                                             bool silu) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[8 * c + e] = 0.f;
-      if (d + 8 * c < n) get8(P.gu, at + 8 * c, v + 8 * c, P.f16);
-    }
+  for (int e = 0; e < 32; e += 2) {
+    const Gate2 ga = gate_of<true>(pair_of(g[e], g[e + 1]), silu);
+    const uint64_t d = pair_of(dh[e], dh[e + 1]), uu = pair_of(u[e], u[e + 1]);
+    of_pair(mul2(mul2(d, uu), ga.da), g[e], g[e + 1]);
+    of_pair(mul2(d, ga.a), u[e], u[e + 1]);
+    of_pair(mul2(ga.a, uu), dh[e], dh[e + 1]);
   }
 }
 
@@ -236,7 +378,8 @@ __global__ void __launch_bounds__(kTgThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStage +
+                                               kTgEpiWarps * kTgWarpStage);
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
   uint64_t* acc_empty = acc_full + 2;
@@ -438,11 +581,24 @@ __global__ void __launch_bounds__(kTgThreads, 1)
     // ================= epilogue =================
     const int grp = (warp - 2) >> 2;  // takes chunks grp, grp + 2, ...
     const int q = warp & 3;           // TMEM lane quarter
+    uint4* stage = reinterpret_cast<uint4*>(smem + C::kStages * C::kStage +
+                                            (warp - 2) * kTgWarpStage);
     int ab = 0;
     uint32_t aph = 0;
     for (int t = first; t < total; t += stride) {
       const TgTile tl = tg_tile(t, P);
       const TgProblem& pr = P.prob[tl.p];
+      const int row0 = tl.m * C::kTileM + static_cast<int>(rank) * 128 + q * 32;
+      const int n0 = tl.n * (KIND == kTgGluFwd ? BN / 2 : BN);
+      const int chunks = row0 < pr.m ? min(KIND == kTgGluFwd ? BN / 64 : BN / 32, (pr.n - n0 + 31) / 32) : 0;
+      Kept kg, ku;
+      if constexpr (KIND == kTgGluBwd) {  // under way while the tile's products end
+        if (grp < chunks) {
+          const Chunk c{lane, row0, pr.m, n0 + 32 * grp, pr.n};
+          kg = request_kept(P, c, 0);
+          ku = request_kept(P, c, 1);
+        }
+      }
       int good = 1;
       if (lane == 0) good = mbar_wait(&acc_full[ab], aph, tmo, abort_flag) ? 1 : 0;
       good = __shfl_sync(0xffffffffu, good, 0);
@@ -456,86 +612,40 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                              static_cast<uint32_t>(ab * C::kAccCols);
-      const int row = tl.m * C::kTileM + static_cast<int>(rank) * 128 + q * 32 + lane;
-      const bool live = row < pr.m;
-      if constexpr (KIND == kTgGluFwd) {
-        for (int c = grp; c < BN / 64; c += 2) {
-          const int d = tl.n * (BN / 2) + 32 * c;  // first feature of the chunk
-          if (d >= pr.n) break;
+      for (int i = grp; i < chunks; i += 2) {
+        const Chunk c{lane, row0, pr.m, n0 + 32 * i, pr.n};
+        if constexpr (KIND == kTgGluFwd) {
           float g[32], u[32];
-          tmem_ld32(tbase + 32 * c, g);
-          tmem_ld32(tbase + BN / 2 + 32 * c, u);
-          if (!live) continue;
+          tmem_ld32(tbase + 32 * i, g);
+          tmem_ld32(tbase + BN / 2 + 32 * i, u);
           if (P.gu != nullptr) {
-            keep32(P, row, d, 0, pr.n, g);
-            keep32(P, row, d, 1, pr.n, u);
+            keep(P, stage, c, 0, g);
+            keep(P, stage, c, 1, u);
           }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) g[e] = gate_of<false>(g[e], P.silu).a * u[e];
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (d + 8 * v < pr.n) put8(pr.out, row * pr.ld_out + d + 8 * v, g + 8 * v, P.f16);
-        }
-      } else if constexpr (KIND == kTgGluBwd) {
-        for (int c = grp; c < BN / 32; c += 2) {
-          const int d = tl.n * BN + 32 * c;
-          if (d >= pr.n) break;
-          float dh[32];
-          tmem_ld32(tbase + 32 * c, dh);
-          if (!live) continue;
-          float g[32], u[32];
-          kept32(P, row, d, 0, pr.n, g);
-          kept32(P, row, d, 1, pr.n, u);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const Gate ga = gate_of<true>(g[e], P.silu);
-            const float uu = u[e];
-            g[e] = dh[e] * uu * ga.da;  // dg
-            u[e] = dh[e] * ga.a;        // du
-            dh[e] = ga.a * uu;          // h
+          glu_forward(g, u, P.silu);
+          put16(stage, c, pr.out, pr.ld_out, g, P.f16);
+        } else if constexpr (KIND == kTgGluBwd) {
+          float dh[32], g[32], u[32];
+          read_kept(P, stage, c, kg, g);
+          read_kept(P, stage, c, ku, u);
+          if (i + 2 < chunks) {
+            const Chunk next{lane, row0, pr.m, c.col + 64, pr.n};
+            kg = request_kept(P, next, 0);
+            ku = request_kept(P, next, 1);
           }
-          const int64_t at = static_cast<int64_t>(row) * 2 * pr.n + d;
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (d + 8 * v < pr.n) {
-              put8(P.dgu, at + 8 * v, g + 8 * v, P.f16);
-              put8(P.dgu, at + pr.n + 8 * v, u + 8 * v, P.f16);
-              if (pr.out != nullptr) put8(pr.out, row * pr.ld_out + d + 8 * v, dh + 8 * v, P.f16);
-            }
-        }
-      } else {
-        for (int c = grp; c < BN / 32; c += 2) {
-          const int n = tl.n * BN + 32 * c;
-          if (n >= pr.n) break;
+          tmem_ld32(tbase + 32 * i, dh);
+          glu_backward(dh, g, u, P.silu);
+          put16(stage, c, P.dgu, 2 * static_cast<int64_t>(pr.n), g, P.f16);
+          put16(stage, c, static_cast<uint16_t*>(P.dgu) + pr.n, 2 * static_cast<int64_t>(pr.n), u,
+                P.f16);
+          if (pr.out != nullptr) put16(stage, c, pr.out, pr.ld_out, dh, P.f16);
+        } else {
           float v[32];
-          tmem_ld32(tbase + 32 * c, v);
-          if (!live) continue;
-          const int64_t at = row * pr.ld_out + n;
-          if (pr.out_f32) {
-            float* o = static_cast<float*>(pr.out) + at;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (n + 4 * k < pr.n) {
-                float4 w = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                if (pr.accumulate) {
-                  const float4 old = *reinterpret_cast<const float4*>(o + 4 * k);
-                  w.x += old.x; w.y += old.y; w.z += old.z; w.w += old.w;
-                }
-                *reinterpret_cast<float4*>(o + 4 * k) = w;
-              }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (n + 8 * k < pr.n) {
-                if (pr.accumulate) {
-                  float old[8];
-                  get8(pr.out, at + 8 * k, old, P.f16);
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) v[8 * k + e] += old[e];
-                }
-                put8(pr.out, at + 8 * k, v + 8 * k, P.f16);
-              }
-          }
+          tmem_ld32(tbase + 32 * i, v);
+          if (pr.out_f32 || pr.accumulate)
+            put32(stage, c, pr.out, pr.ld_out, v, pr.out_f32, pr.accumulate, P.f16);
+          else
+            put16(stage, c, pr.out, pr.ld_out, v, P.f16);
         }
       }
       tc_fence_before();
