@@ -18,9 +18,9 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = ["router.cu", "router_tc.cu", "permute.cu", "grouped_gemm.cu", "stream_gemm.cu",
            "combine.cu", "quant.cu", "health.cu", "moe_ffn.cu",
-           "act8.cu", "norm.cu", "train_gemm.cu", "train.cu"]
+           "act8.cu", "norm.cu", "train_gemm.cu", "train_small.cu", "train.cu"]
 HEADERS = ["common.cuh", "internal.h", "permute_impl.cuh", "warp_mma.cuh", "act8.cuh",
-           "train_internal.h"]
+           "train_internal.h", "train_tile.cuh"]
 INTERFACES = ["moe_ffn.h", "moe_train.h"]
 LIB = os.path.join(PKG, "libmoeffn.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

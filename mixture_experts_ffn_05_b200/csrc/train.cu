@@ -174,12 +174,20 @@ TgShape pick_shape(const Product* pr, int n, bool glu_fwd) {
   return kTgOne64;
 }
 
+// Few tokens: one product whose tiles of 128 features all run at one time.
+bool small_product(const Product& pr, bool glu_fwd) {
+  return !pr.a.mn && !pr.out_f32 && !pr.accumulate &&
+         ceil_div(pr.m, 128) * ceil_div(pr.n, glu_fwd ? 64 : 128) <= kTsMostCtas;
+}
+
 moe_status_t run_products(const Product* pr, int n, TgParams p, cudaStream_t s, bool pdl) {
   const int sms = device_sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
   const bool glu_fwd = p.kind == kTgGluFwd;
-  const TgShape shape = pick_shape(pr, n, glu_fwd);
-  const int tm = tg_tile_m(shape), tn = tg_tile_n(shape);
+  const bool small = n == 1 && small_product(pr[0], glu_fwd);
+  const TgShape shape = small ? kTgOne128 : pick_shape(pr, n, glu_fwd);
+  const int nt = ts_tokens(pr[0].m);
+  const int tm = small ? nt : tg_tile_m(shape), tn = tg_tile_n(shape);
   const int b_rows = shape == kTgPair256 ? 128 : tn;  // B rows that one CTA loads
   TgMaps maps{};
   for (int i = 0; i < n; ++i) {
@@ -196,7 +204,7 @@ moe_status_t run_products(const Product* pr, int n, TgParams p, cudaStream_t s, 
     q.ld_out = pr[i].ld_out;
     q.out_f32 = pr[i].out_f32;
     q.accumulate = pr[i].accumulate;
-    if (!map_operand(&maps.a[i], pr[i].a, pr[i].m, pr[i].k, 128)) return MOE_ERR_CUDA;
+    if (!map_operand(&maps.a[i], pr[i].a, pr[i].m, pr[i].k, small ? nt : 128)) return MOE_ERR_CUDA;
     const bool ok = glu_fwd ? map_gate_up(&maps.b[i], pr[i].b.p, pr[i].n, pr[i].k,
                                           shape == kTgPair256 ? 128 : tn / 2)
                             : map_operand(&maps.b[i], pr[i].b, pr[i].n, pr[i].k, b_rows);
@@ -207,6 +215,7 @@ moe_status_t run_products(const Product* pr, int n, TgParams p, cudaStream_t s, 
     maps.b[i] = maps.b[0];
   }
   p.nprob = n;
+  if (small) return cuda_status(launch_train_small(maps, p, nt, s, pdl));
   return cuda_status(launch_train_gemm(shape, maps, p, sms, s, pdl));
 }
 
@@ -393,13 +402,20 @@ moe_status_t moe_mlp_backward(const moe_mlp_config_t* cfg, int32_t T, const moe_
   if ((st = run_products(&dh, 1, p, s, false)) != MOE_OK) return st;
   Product out[3];
   int n = 0;
-  if (dx != nullptr)
+  if (dx != nullptr) {
     out[n++] = Product{T, H, 2 * D, {dgu, 2 * D, false}, {w_gate_up, H, true},
                        dx->data, dx->ld, 0, 0};
+    if (small_product(out[0], false)) {  // a launch of its own, whose K loop is split
+      if ((st = run_products(out, 1, mlp_params(cfg, kTgStore, nullptr, ws), s, true)) != MOE_OK)
+        return st;
+      n = 0;
+    }
+  }
   if (dw_gate_up != nullptr)
     out[n++] = Product{2 * D, H, T, {dgu, 2 * D, true}, {x16, ldx, true}, dw_gate_up, H, f32, acc};
   if (dw_down != nullptr)
     out[n++] = Product{H, D, T, {dy->data, dy->ld, true}, {h, D, true}, dw_down, D, f32, acc};
+  if (n == 0) return MOE_OK;
   return run_products(out, n, mlp_params(cfg, kTgStore, nullptr, ws), s, true);
 }
 

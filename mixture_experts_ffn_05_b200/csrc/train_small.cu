@@ -1,0 +1,347 @@
+// The products of the gated MLP for few tokens, where the weights' bytes and the latency of the
+// K loop bind and not the tensor cores: C[t][f] = sum_k X[t][k] W[f][k] with the weights as the
+// M operand (128 features a tile, every TMEM lane in use) and up to 128 tokens as N.
+//
+// A cluster of 1, 2, 4 or 8 CTAs shares a tile and splits its K steps, so that the weights of
+// one product stream through all SMs at once; with whole K loops 66 CTAs of 44 steps took 21 us
+// for the 24 MB of a gate_up product at 8 tokens.  Each CTA leaves its fp32 sums in its own
+// shared memory as [token][128 features]; the CTAs then take tokens in turn, add the partial
+// sums in rank order through distributed shared memory (deterministic) and apply the epilogue,
+// four neighbouring features a lane, so that a warp writes 128 to 256 contiguous bytes.
+//
+// Weights do not depend on the kernel before: the first ring fill requests them before the
+// dependency wait, and the ring takes less than half of an SM, so that the next product's
+// weights already come in while this one runs.
+#include "train_internal.h"
+#include "train_tile.cuh"
+
+namespace moe {
+
+constexpr int kTsThreads = 320;        // producer, MMA, 8 epilogue warps
+constexpr int kTsWeightBytes = 16384;  // 128 features x 64 K elements
+constexpr int kTsRingBytes = 96 * 1024;
+constexpr int kTsMaxStages = 8;
+
+// A token's sums of four neighbouring features over the cluster's CTAs, in rank order.
+__device__ __forceinline__ void cluster_sum4(float (&v)[4], const float* mine, int splits) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = 0.f;
+  for (int c = 0; c < splits; ++c) {
+    float p[4];
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(p[0]), "=f"(p[1]), "=f"(p[2]), "=f"(p[3])
+                 : "r"(cluster_addr(mine, c))
+                 : "memory");
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += p[e];
+  }
+}
+
+__device__ __forceinline__ void put4(void* base, int64_t i, const float (&v)[4], bool f16) {
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) =
+      f16 ? make_uint2(pack2_f16(v[0], v[1]), pack2_f16(v[2], v[3]))
+          : make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+}
+
+// A group of 32 features is eight lanes' four values; every lane takes part.
+template <bool INT8>
+__device__ __forceinline__ void keep4(const TgParams& P, const float (&v)[4], int64_t row, int half,
+                                      int f, int n, bool live) {
+  uint32_t m = amax_bits(v);
+#pragma unroll
+  for (int o = 1; o < 8; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int b = scale_byte<INT8>(m);
+  if (!live) return;
+  const int groups = (n + kGroup8 - 1) / kGroup8;
+  if (f % kGroup8 == 0)
+    P.gu_scales[(row * 2 + half) * groups + f / kGroup8] = static_cast<uint8_t>(b);
+  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(P.gu) + row * P.ld_gu +
+                               static_cast<int64_t>(half) * n + f) =
+      encode4<INT8>(v[0], v[1], v[2], v[3], scale_inverse(b));
+}
+
+__device__ __forceinline__ void kept4(const TgParams& P, float (&v)[4], int64_t row, int half, int f,
+                                      int n) {
+  const int64_t at = row * P.ld_gu + static_cast<int64_t>(half) * n + f;
+  if (fmt_bytes(P.gu_fmt) == 1) {
+    const int groups = (n + kGroup8 - 1) / kGroup8;
+    const float s = scale_value(P.gu_scales[(row * 2 + half) * groups + f / kGroup8]);
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(P.gu) + at);
+    if (P.gu_fmt == kFmtInt8)
+      decode4<true>(w, s, v);
+    else
+      decode4<false>(w, s, v);
+    return;
+  }
+  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(P.gu) + at);
+  float t[8];
+  if (P.f16)
+    unpack8_f16(make_uint4(w.x, w.y, 0u, 0u), t);
+  else
+    unpack8(make_uint4(w.x, w.y, 0u, 0u), t);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = t[e];
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kTsThreads, 2)
+    train_small_kernel(const __grid_constant__ TgMaps maps, const __grid_constant__ TgParams P,
+                       int nt, int stages) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t full[kTsMaxStages], empty[kTsMaxStages], done[1];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const TgProblem& pr = P.prob[0];
+  const int stage_bytes = kTsWeightBytes + nt * 128;
+  uint32_t splits;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
+  const uint32_t rank = cluster_ctarank();
+  const int tile = static_cast<int>(blockIdx.x / splits);
+  const int fb = tile % pr.n_tiles, tb = tile / pr.n_tiles;  // feature and token tile
+  const int k_first = pr.k_steps * static_cast<int>(rank) / static_cast<int>(splits);
+  const int k_end = pr.k_steps * static_cast<int>(rank + 1) / static_cast<int>(splits);
+  const int steps = k_end - k_first;
+  const uint32_t cols = nt <= 32 ? 32 : nt <= 64 ? 64 : 128;  // TMEM columns
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(done, 1);
+    mbar_fence_init();
+    abort_flag = 0;
+    tma_prefetch_map(&maps.a[0]);
+    tma_prefetch_map(&maps.b[0]);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  const uint64_t tmo = P.timeout_ns;
+  pdl_trigger();
+
+  if (warp == 0) {
+    // ================= TMA producer =================
+    if (lane == 0) {
+      const uint64_t keep_w = policy_evict_first(), keep_x = policy_evict_last();
+      auto weights = [&](int k, int s) {
+        uint8_t* dst = smem + s * stage_bytes;
+        const int k0 = (k_first + k) * 64;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        if constexpr (KIND == kTgGluFwd) {
+          tma_load_3d(dst, &maps.b[0], &full[s], k0, fb * 64, 0, keep_w);
+          tma_load_3d(dst + kTsWeightBytes / 2, &maps.b[0], &full[s], k0, fb * 64, 1, keep_w);
+        } else if (pr.b_mn) {
+          tma_load_2d(dst, &maps.b[0], &full[s], fb * 128, k0, keep_w);
+          tma_load_2d(dst + kTsWeightBytes / 2, &maps.b[0], &full[s], fb * 128 + 64, k0, keep_w);
+        } else {
+          tma_load_2d(dst, &maps.b[0], &full[s], k0, fb * 128, keep_w);
+        }
+      };
+      auto tokens = [&](int k, int s) {
+        tma_load_2d(smem + s * stage_bytes + kTsWeightBytes, &maps.a[0], &full[s],
+                    (k_first + k) * 64, tb * nt, keep_x);
+      };
+      const int ahead = steps < stages ? steps : stages;
+      for (int k = 0; k < ahead; ++k) weights(k, k);
+      pdl_wait();
+      for (int k = 0; k < ahead; ++k) tokens(k, k);
+      int s = 0, last = ahead;
+      uint32_t phase = 0;
+      for (int k = ahead; k < steps; ++k) {
+        if (!mbar_wait(&empty[s], phase, tmo, &abort_flag)) {
+          record_status(P.status, kStatusTimeout);
+          abort_flag = 1;
+          break;
+        }
+        weights(k, s);
+        tokens(k, s);
+        last = k + 1;
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+      // every copy lands before the CTA winds down, whatever else happened
+      for (int k = last > stages ? last - stages : 0; k < last; ++k)
+        mbar_wait(&full[k % stages], static_cast<uint32_t>(k / stages) & 1u, tmo, nullptr);
+    }
+  } else if (warp == 1) {
+    // ================= MMA issuer =================
+    if (lane == 0) {
+      const uint32_t idesc = (P.f16 ? idesc_f16_f32(128, nt) : idesc_bf16_f32(128, nt)) |
+                             (pr.b_mn ? 1u << 15 : 0u);
+      const uint64_t wstep = pr.b_mn ? 2048 >> 4 : 32 >> 4;
+      int s = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int k = 0; k < steps; ++k) {
+        if (!mbar_wait(&full[s], phase, tmo, &abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sw = smem_u32(smem + s * stage_bytes);
+        uint64_t wd = pr.b_mn ? sdesc_mn_sw128(sw) : sdesc_k_sw128(sw);
+        uint64_t xd = sdesc_k_sw128(sw + kTsWeightBytes);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          umma_bf16(tmem_base, wd, xd, idesc, k > 0 || kk > 0 ? 1u : 0u);
+          wd += wstep;
+          xd += 32 >> 4;
+        }
+        umma_commit(&empty[s]);
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        record_status(P.status, kStatusTimeout);
+        abort_flag = 1;
+      }
+      umma_commit(done);  // also after a timeout: what was issued ends before TMEM is released
+    }
+  } else {
+    // ================= sums to shared memory =================
+    pdl_wait();  // the epilogue below reads and overwrites what the kernel before uses
+    int good = 1;
+    if (lane == 0) good = mbar_wait(done, 0, tmo, nullptr) ? 1 : 0;
+    good = __shfl_sync(0xffffffffu, good, 0);
+    if (!good) {
+      if (lane == 0) {
+        record_status(P.status, kStatusTimeout);
+        abort_flag = 1;
+      }
+    } else {
+      // every copy has landed and every MMA has read it: the ring is free
+      tc_fence_after();
+      const int q = warp & 3;
+      float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
+      for (int c = (warp - 2) >> 2; 16 * c < nt; c += 2) {
+        float v[16];
+        tmem_ld16(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + 16 * c, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(16 * c + j) * 128] = v[j];
+      }
+      tc_fence_before();
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // all CTAs' sums are in place
+
+  if (warp >= 2 && !abort_flag) {
+    const int f0 = KIND == kTgGluFwd ? fb * 64 + 4 * (lane & 15) : fb * 128 + 4 * lane;
+    const int tokens = min(nt, pr.m - tb * nt);
+    for (int t = static_cast<int>(rank) + static_cast<int>(splits) * (warp - 2); t < tokens;
+         t += 8 * static_cast<int>(splits)) {
+      float v[4];
+      cluster_sum4(v, reinterpret_cast<const float*>(smem) + t * 128 + 4 * lane,
+                   static_cast<int>(splits));
+      const int64_t row = static_cast<int64_t>(tb) * nt + t;
+      const bool live = f0 < pr.n;  // n is a multiple of 8
+      if constexpr (KIND == kTgGluFwd) {  // lanes 0-15 hold gate, 16-31 up
+        const int half = lane >> 4;
+        if (P.gu != nullptr) {
+          if (P.gu_fmt == kFmtInt8)
+            keep4<true>(P, v, row, half, f0, pr.n, live);
+          else if (P.gu_fmt == kFmtE4m3)
+            keep4<false>(P, v, row, half, f0, pr.n, live);
+          else if (live)
+            put4(P.gu, row * P.ld_gu + static_cast<int64_t>(half) * pr.n + f0, v, P.f16);
+        }
+        float u[4], h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = __shfl_xor_sync(0xffffffffu, v[e], 16);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+          of_pair(mul2(gate_of<false>(pair_of(v[e], v[e + 1]), P.silu).a, pair_of(u[e], u[e + 1])),
+                  h[e], h[e + 1]);
+        if (live && half == 0) put4(pr.out, row * pr.ld_out + f0, h, P.f16);
+      } else if (live) {
+        if constexpr (KIND == kTgGluBwd) {
+          float g[4], u[4];
+          kept4(P, g, row, 0, f0, pr.n);
+          kept4(P, u, row, 1, f0, pr.n);
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const Gate2 ga = gate_of<true>(pair_of(g[e], g[e + 1]), P.silu);
+            const uint64_t d = pair_of(v[e], v[e + 1]), uu = pair_of(u[e], u[e + 1]);
+            of_pair(mul2(mul2(d, uu), ga.da), g[e], g[e + 1]);
+            of_pair(mul2(d, ga.a), u[e], u[e + 1]);
+            of_pair(mul2(ga.a, uu), v[e], v[e + 1]);
+          }
+          const int64_t at = row * 2 * pr.n + f0;
+          put4(P.dgu, at, g, P.f16);
+          put4(P.dgu, at + pr.n, u, P.f16);
+          if (pr.out != nullptr) put4(pr.out, row * pr.ld_out + f0, v, P.f16);
+        } else {
+          put4(pr.out, row * pr.ld_out + f0, v, P.f16);
+        }
+      }
+    }
+  }
+  // ---- teardown: no CTA exits while its peers may still read its sums
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, cols);
+  }
+}
+
+// CTAs that share a tile: as many as the SMs hold at one time, with at least four K steps each.
+int train_small_splits(int64_t tiles, int k_steps) {
+  int c = 1;
+  while (c < 8 && tiles * 2 * c <= kTsMostCtas && k_steps >= 8 * c) c *= 2;
+  return c;
+}
+
+template <int KIND>
+static cudaError_t launch_ts(const TgMaps& maps, const TgParams& p, int nt, cudaStream_t s,
+                             bool pdl) {
+  const int stage = kTsWeightBytes + nt * 128;
+  const int stages = kTsRingBytes / stage < kTsMaxStages ? kTsRingBytes / stage : kTsMaxStages;
+  const int smem = 1024 + kTsRingBytes;
+  auto kernel = train_small_kernel<KIND>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>(p.prob[0].m_tiles) * p.prob[0].n_tiles;
+  const int splits = train_small_splits(tiles, p.prob[0].k_steps);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
+  cfg.blockDim = dim3(kTsThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, p, nt, stages);
+}
+
+cudaError_t launch_train_small(const TgMaps& maps, const TgParams& p, int nt, cudaStream_t s,
+                               bool pdl) {
+  switch (p.kind) {
+    case kTgStore: return launch_ts<kTgStore>(maps, p, nt, s, pdl);
+    case kTgGluFwd: return launch_ts<kTgGluFwd>(maps, p, nt, s, pdl);
+    case kTgGluBwd: return launch_ts<kTgGluBwd>(maps, p, nt, s, pdl);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace moe
