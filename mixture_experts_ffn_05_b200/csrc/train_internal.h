@@ -101,7 +101,7 @@ cudaError_t launch_train_gemm(TgShape shape, const TgMaps& maps, const TgParams&
 // The same for few tokens (prob[0] alone): tiles of 128 features (GLU forward: 64, gate and up)
 // by nt tokens, nt a multiple of 16 up to 128, their K steps split over a cluster.  Taken while
 // its tiles fit the GPU at one time.
-constexpr int kTsMostCtas = 160;
+constexpr int kTsMostCtas = kB200Sms;
 constexpr int ts_tokens(int64_t T) { return T >= 128 ? 128 : static_cast<int>((T + 15) / 16 * 16); }
 cudaError_t launch_train_small(const TgMaps& maps, const TgParams& p, int nt, cudaStream_t s,
                                bool pdl);

@@ -6,7 +6,7 @@
 // one product stream through all SMs at once; with whole K loops 66 CTAs of 44 steps took 21 us
 // for the 24 MB of a gate_up product at 8 tokens.  Each CTA leaves its fp32 sums in its own
 // shared memory as [token][128 features]; the CTAs then take tokens in turn, add the partial
-// sums in rank order through distributed shared memory (deterministic) and apply the epilogue,
+// sums in a fixed order through distributed shared memory and apply the epilogue,
 // four neighbouring features a lane, so that a warp writes 128 to 256 contiguous bytes.
 //
 // Weights do not depend on the kernel before: the first ring fill requests them before the
@@ -19,22 +19,40 @@ namespace moe {
 
 constexpr int kTsThreads = 320;        // producer, MMA, 8 epilogue warps
 constexpr int kTsWeightBytes = 16384;  // 128 features x 64 K elements
-constexpr int kTsRingBytes = 96 * 1024;
+constexpr int kTsRingBytes = 96 * 1024;  // two CTAs an SM
 constexpr int kTsMaxStages = 8;
 
-// A token's sums of four neighbouring features over the cluster's CTAs, in rank order.
-__device__ __forceinline__ void cluster_sum4(float (&v)[4], const float* mine, int splits) {
+// N tokens' sums of four neighbouring features over the cluster's CTAs; `mine` + i * `step`
+// floats is token i's place.  All loads are under way at once, and each CTA begins with its own
+// sums, so that the cluster does not read one CTA's memory all at a time (in rank order the
+// sums of 64 tokens over 8 CTAs took 7 us).  A token is always summed by the same rank, so the
+// order is fixed.
+template <int SPLITS, int N>
+__device__ __forceinline__ void cluster_sums(float (&v)[N][4], const float* mine, int step,
+                                             int count, uint32_t rank) {
+  float p[SPLITS][N][4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = 0.f;
-  for (int c = 0; c < splits; ++c) {
-    float p[4];
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(p[0]), "=f"(p[1]), "=f"(p[2]), "=f"(p[3])
-                 : "r"(cluster_addr(mine, c))
-                 : "memory");
+  for (int c = 0; c < SPLITS; ++c) {
+    const uint32_t from = cluster_addr(mine, (rank + c) % SPLITS);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += p[e];
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[c][i][e] = 0.f;
+      if (i < count)
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(p[c][i][0]), "=f"(p[c][i][1]), "=f"(p[c][i][2]), "=f"(p[c][i][3])
+                     : "r"(from + static_cast<uint32_t>(i * step * 4))
+                     : "memory");
+    }
   }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[i][e] = p[0][i][e];
+#pragma unroll
+      for (int c = 1; c < SPLITS; ++c) v[i][e] += p[c][i][e];
+    }
 }
 
 __device__ __forceinline__ void put4(void* base, int64_t i, const float (&v)[4], bool f16) {
@@ -83,7 +101,7 @@ __device__ __forceinline__ void kept4(const TgParams& P, float (&v)[4], int64_t 
   for (int e = 0; e < 4; ++e) v[e] = t[e];
 }
 
-template <int KIND>
+template <int KIND, int SPLITS>
 __global__ void __launch_bounds__(kTsThreads, 2)
     train_small_kernel(const __grid_constant__ TgMaps maps, const __grid_constant__ TgParams P,
                        int nt, int stages) {
@@ -96,13 +114,12 @@ __global__ void __launch_bounds__(kTsThreads, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const TgProblem& pr = P.prob[0];
   const int stage_bytes = kTsWeightBytes + nt * 128;
-  uint32_t splits;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
+  constexpr int kBatch = SPLITS >= 4 ? 2 : 4;  // tokens a warp sums at a time
   const uint32_t rank = cluster_ctarank();
-  const int tile = static_cast<int>(blockIdx.x / splits);
+  const int tile = static_cast<int>(blockIdx.x / SPLITS);
   const int fb = tile % pr.n_tiles, tb = tile / pr.n_tiles;  // feature and token tile
-  const int k_first = pr.k_steps * static_cast<int>(rank) / static_cast<int>(splits);
-  const int k_end = pr.k_steps * static_cast<int>(rank + 1) / static_cast<int>(splits);
+  const int k_first = pr.k_steps * static_cast<int>(rank) / SPLITS;
+  const int k_end = pr.k_steps * static_cast<int>(rank + 1) / SPLITS;
   const int steps = k_end - k_first;
   const uint32_t cols = nt <= 32 ? 32 : nt <= 64 ? 64 : 128;  // TMEM columns
 
@@ -241,50 +258,64 @@ __global__ void __launch_bounds__(kTsThreads, 2)
   if (warp >= 2 && !abort_flag) {
     const int f0 = KIND == kTgGluFwd ? fb * 64 + 4 * (lane & 15) : fb * 128 + 4 * lane;
     const int tokens = min(nt, pr.m - tb * nt);
-    for (int t = static_cast<int>(rank) + static_cast<int>(splits) * (warp - 2); t < tokens;
-         t += 8 * static_cast<int>(splits)) {
-      float v[4];
-      cluster_sum4(v, reinterpret_cast<const float*>(smem) + t * 128 + 4 * lane,
-                   static_cast<int>(splits));
-      const int64_t row = static_cast<int64_t>(tb) * nt + t;
-      const bool live = f0 < pr.n;  // n is a multiple of 8
-      if constexpr (KIND == kTgGluFwd) {  // lanes 0-15 hold gate, 16-31 up
-        const int half = lane >> 4;
-        if (P.gu != nullptr) {
-          if (P.gu_fmt == kFmtInt8)
-            keep4<true>(P, v, row, half, f0, pr.n, live);
-          else if (P.gu_fmt == kFmtE4m3)
-            keep4<false>(P, v, row, half, f0, pr.n, live);
-          else if (live)
-            put4(P.gu, row * P.ld_gu + static_cast<int64_t>(half) * pr.n + f0, v, P.f16);
-        }
-        float u[4], h[4];
+    const bool live = f0 < pr.n;  // n is a multiple of 8
+    constexpr int step = 8 * SPLITS;
+    for (int t0 = static_cast<int>(rank) + SPLITS * (warp - 2); t0 < tokens;
+         t0 += kBatch * step) {
+      const int64_t row0 = static_cast<int64_t>(tb) * nt + t0;
+      const int count = min(kBatch, (tokens - t0 + step - 1) / step);
+      float v[kBatch][4];
+      float g[KIND == kTgGluBwd ? kBatch : 1][4], u[KIND == kTgGluBwd ? kBatch : 1][4];
+      if constexpr (KIND == kTgGluBwd) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = __shfl_xor_sync(0xffffffffu, v[e], 16);
-#pragma unroll
-        for (int e = 0; e < 4; e += 2)
-          of_pair(mul2(gate_of<false>(pair_of(v[e], v[e + 1]), P.silu).a, pair_of(u[e], u[e + 1])),
-                  h[e], h[e + 1]);
-        if (live && half == 0) put4(pr.out, row * pr.ld_out + f0, h, P.f16);
-      } else if (live) {
-        if constexpr (KIND == kTgGluBwd) {
-          float g[4], u[4];
-          kept4(P, g, row, 0, f0, pr.n);
-          kept4(P, u, row, 1, f0, pr.n);
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const Gate2 ga = gate_of<true>(pair_of(g[e], g[e + 1]), P.silu);
-            const uint64_t d = pair_of(v[e], v[e + 1]), uu = pair_of(u[e], u[e + 1]);
-            of_pair(mul2(mul2(d, uu), ga.da), g[e], g[e + 1]);
-            of_pair(mul2(d, ga.a), u[e], u[e + 1]);
-            of_pair(mul2(ga.a, uu), v[e], v[e + 1]);
+        for (int i = 0; i < kBatch; ++i)
+          if (i < count && live) {
+            kept4(P, g[i], row0 + i * step, 0, f0, pr.n);
+            kept4(P, u[i], row0 + i * step, 1, f0, pr.n);
           }
-          const int64_t at = row * 2 * pr.n + f0;
-          put4(P.dgu, at, g, P.f16);
-          put4(P.dgu, at + pr.n, u, P.f16);
-          if (pr.out != nullptr) put4(pr.out, row * pr.ld_out + f0, v, P.f16);
-        } else {
-          put4(pr.out, row * pr.ld_out + f0, v, P.f16);
+      }
+      cluster_sums<SPLITS>(v, reinterpret_cast<const float*>(smem) + t0 * 128 + 4 * lane,
+                           step * 128, count, rank);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (i >= count) break;
+        const int64_t row = row0 + i * step;
+        if constexpr (KIND == kTgGluFwd) {  // lanes 0-15 hold gate, 16-31 up
+          const int half = lane >> 4;
+          if (P.gu != nullptr) {
+            if (P.gu_fmt == kFmtInt8)
+              keep4<true>(P, v[i], row, half, f0, pr.n, live);
+            else if (P.gu_fmt == kFmtE4m3)
+              keep4<false>(P, v[i], row, half, f0, pr.n, live);
+            else if (live)
+              put4(P.gu, row * P.ld_gu + static_cast<int64_t>(half) * pr.n + f0, v[i], P.f16);
+          }
+          float up[4], h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) up[e] = __shfl_xor_sync(0xffffffffu, v[i][e], 16);
+#pragma unroll
+          for (int e = 0; e < 4; e += 2)
+            of_pair(mul2(gate_of<false>(pair_of(v[i][e], v[i][e + 1]), P.silu).a,
+                         pair_of(up[e], up[e + 1])),
+                    h[e], h[e + 1]);
+          if (live && half == 0) put4(pr.out, row * pr.ld_out + f0, h, P.f16);
+        } else if (live) {
+          if constexpr (KIND == kTgGluBwd) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const Gate2 ga = gate_of<true>(pair_of(g[i][e], g[i][e + 1]), P.silu);
+              const uint64_t d = pair_of(v[i][e], v[i][e + 1]), uu = pair_of(u[i][e], u[i][e + 1]);
+              of_pair(mul2(mul2(d, uu), ga.da), g[i][e], g[i][e + 1]);
+              of_pair(mul2(d, ga.a), u[i][e], u[i][e + 1]);
+              of_pair(mul2(ga.a, uu), v[i][e], v[i][e + 1]);
+            }
+            const int64_t at = row * 2 * pr.n + f0;
+            put4(P.dgu, at, g[i], P.f16);
+            put4(P.dgu, at + pr.n, u[i], P.f16);
+            if (pr.out != nullptr) put4(pr.out, row * pr.ld_out + f0, v[i], P.f16);
+          } else {
+            put4(pr.out, row * pr.ld_out + f0, v[i], P.f16);
+          }
         }
       }
     }
@@ -299,32 +330,30 @@ __global__ void __launch_bounds__(kTsThreads, 2)
   }
 }
 
-// CTAs that share a tile: as many as the SMs hold at one time, with at least four K steps each.
-int train_small_splits(int64_t tiles, int k_steps) {
+// CTAs that share a tile: as many as the SMs hold at one time, with at least two K steps each.
+static int train_small_splits(int64_t tiles, int k_steps) {
   int c = 1;
-  while (c < 8 && tiles * 2 * c <= kTsMostCtas && k_steps >= 8 * c) c *= 2;
+  while (c < 8 && tiles * 2 * c <= kTsMostCtas && k_steps >= 4 * c) c *= 2;
   return c;
 }
 
-template <int KIND>
+template <int KIND, int SPLITS>
 static cudaError_t launch_ts(const TgMaps& maps, const TgParams& p, int nt, cudaStream_t s,
                              bool pdl) {
   const int stage = kTsWeightBytes + nt * 128;
   const int stages = kTsRingBytes / stage < kTsMaxStages ? kTsRingBytes / stage : kTsMaxStages;
   const int smem = 1024 + kTsRingBytes;
-  auto kernel = train_small_kernel<KIND>;
+  auto kernel = train_small_kernel<KIND, SPLITS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>(p.prob[0].m_tiles) * p.prob[0].n_tiles;
-  const int splits = train_small_splits(tiles, p.prob[0].k_steps);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.prob[0].m_tiles * p.prob[0].n_tiles * SPLITS));
   cfg.blockDim = dim3(kTsThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.x = SPLITS;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -334,12 +363,24 @@ static cudaError_t launch_ts(const TgMaps& maps, const TgParams& p, int nt, cuda
   return cudaLaunchKernelEx(&cfg, kernel, maps, p, nt, stages);
 }
 
+template <int KIND>
+static cudaError_t launch_kind(const TgMaps& maps, const TgParams& p, int nt, cudaStream_t s,
+                               bool pdl) {
+  switch (train_small_splits(static_cast<int64_t>(p.prob[0].m_tiles) * p.prob[0].n_tiles,
+                             p.prob[0].k_steps)) {
+    case 1: return launch_ts<KIND, 1>(maps, p, nt, s, pdl);
+    case 2: return launch_ts<KIND, 2>(maps, p, nt, s, pdl);
+    case 4: return launch_ts<KIND, 4>(maps, p, nt, s, pdl);
+    default: return launch_ts<KIND, 8>(maps, p, nt, s, pdl);
+  }
+}
+
 cudaError_t launch_train_small(const TgMaps& maps, const TgParams& p, int nt, cudaStream_t s,
                                bool pdl) {
   switch (p.kind) {
-    case kTgStore: return launch_ts<kTgStore>(maps, p, nt, s, pdl);
-    case kTgGluFwd: return launch_ts<kTgGluFwd>(maps, p, nt, s, pdl);
-    case kTgGluBwd: return launch_ts<kTgGluBwd>(maps, p, nt, s, pdl);
+    case kTgStore: return launch_kind<kTgStore>(maps, p, nt, s, pdl);
+    case kTgGluFwd: return launch_kind<kTgGluFwd>(maps, p, nt, s, pdl);
+    case kTgGluBwd: return launch_kind<kTgGluBwd>(maps, p, nt, s, pdl);
   }
   return cudaErrorInvalidValue;
 }
