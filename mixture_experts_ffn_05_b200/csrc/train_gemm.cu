@@ -375,12 +375,11 @@ __global__ void __launch_bounds__(kTgThreads, 1)
 
   if (warp == 0) {
     // ================= TMA producer =================
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t pol = policy_evict_last();
       int stage = 0;
       uint32_t phase = 0;
-      int armed[C::kStages];
-      for (int i = 0; i < C::kStages; ++i) armed[i] = -1;
+      int64_t fills = 0;
       bool ok = true;
       for (int t = first; t < total && ok; t += stride) {
         const TgTile tl = tg_tile(t, P);
@@ -391,7 +390,9 @@ __global__ void __launch_bounds__(kTgThreads, 1)
         // GLU forward: the tile's columns are BN / 2 features, gate and up rows of each
         const int n0 = KIND == kTgGluFwd ? tl.n * (BN / 2)
                                          : tl.n * BN + (PAIR ? static_cast<int>(rank) * 128 : 0);
-        for (int ks = 0; ks < pr.k_steps; ++ks) {
+        const int k_steps = pr.k_steps;
+        const bool a_mn = pr.a_mn, b_mn = pr.b_mn;
+        for (int ks = 0; ks < k_steps; ++ks) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, tmo, abort_flag)) {
             ok = false;
             break;
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
             else
               tma_load_2d(dst, m, &full[stage], c0, c1, pol);
           };
-          if (pr.a_mn) {
+          if (a_mn) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) load2(sa + j * 8192, ma, m0 + 64 * j, k0);
           } else {
@@ -420,13 +421,13 @@ __global__ void __launch_bounds__(kTgThreads, 1)
               tma_load_3d(sb, mb, &full[stage], k0, n0, 0, pol);
               tma_load_3d(sb + C::kBBytes / 2, mb, &full[stage], k0, n0, 1, pol);
             }
-          } else if (pr.b_mn) {
+          } else if (b_mn) {
 #pragma unroll
             for (int j = 0; j < C::kBRows / 64; ++j) load2(sb + j * 8192, mb, n0 + 64 * j, k0);
           } else {
             load2(sb, mb, k0, n0);
           }
-          armed[stage] = static_cast<int>(phase);
+          ++fills;
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
@@ -439,13 +440,13 @@ __global__ void __launch_bounds__(kTgThreads, 1)
         // every copy already issued lands before the CTA winds down (PAIR: the leader's
         // barriers count both CTAs' copies)
         if (!PAIR || leader)
-          for (int i = 0; i < C::kStages; ++i)
-            if (armed[i] >= 0) mbar_wait(&full[i], static_cast<uint32_t>(armed[i]), tmo, nullptr);
+          for (int64_t i = fills > C::kStages ? fills - C::kStages : 0; i < fills; ++i)
+            mbar_wait(&full[i % C::kStages], static_cast<uint32_t>(i / C::kStages) & 1u, tmo, nullptr);
       }
     }
   } else if (warp == 1) {
     // ================= MMA issuer (PAIR: the leader's, for both CTAs) =================
-    if (lane == 0 && leader) {
+    if (leader && elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       int ab = 0;
@@ -456,26 +457,28 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       for (int t = first; t < total && ok; t += stride) {
         const TgTile tl = tg_tile(t, P);
         const TgProblem& pr = P.prob[tl.p];
+        const int k_steps = pr.k_steps;
+        const bool a_mn = pr.a_mn, b_mn = pr.b_mn;
         const uint32_t idesc = (P.f16 ? idesc_f16_f32(C::kTileM, BN) : idesc_bf16_f32(C::kTileM, BN)) |
-                               (pr.a_mn ? 1u << 15 : 0u) | (pr.b_mn ? 1u << 16 : 0u);
+                               (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
         // 16 K elements: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
-        const uint64_t astep = pr.a_mn ? 2048 >> 4 : 32 >> 4;
-        const uint64_t bstep = pr.b_mn ? 2048 >> 4 : 32 >> 4;
+        const uint64_t astep = a_mn ? 2048 >> 4 : 32 >> 4;
+        const uint64_t bstep = b_mn ? 2048 >> 4 : 32 >> 4;
         if (!mbar_wait(&acc_empty[ab], aph ^ 1u, tmo, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(ab * C::kAccCols);
-        for (int ks = 0; ks < pr.k_steps; ++ks) {
+        for (int ks = 0; ks < k_steps; ++ks) {
           if (!mbar_wait(&full[stage], phase, tmo, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t sa = smem_u32(smem + stage * C::kStage);
-          uint64_t ad = pr.a_mn ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
-          uint64_t bd = pr.b_mn ? sdesc_mn_sw128(sa + C::kABytes) : sdesc_k_sw128(sa + C::kABytes);
+          uint64_t ad = a_mn ? sdesc_mn_sw128(sa) : sdesc_k_sw128(sa);
+          uint64_t bd = b_mn ? sdesc_mn_sw128(sa + C::kABytes) : sdesc_k_sw128(sa + C::kABytes);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint32_t acc = (ks > 0 || kk > 0) ? 1u : 0u;

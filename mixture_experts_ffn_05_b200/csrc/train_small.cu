@@ -147,8 +147,9 @@ __global__ void __launch_bounds__(kTsThreads, 2)
 
   if (warp == 0) {
     // ================= TMA producer =================
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t keep_w = policy_evict_first(), keep_x = policy_evict_last();
+      const bool w_mn = pr.b_mn;
       auto weights = [&](int k, int s) {
         uint8_t* dst = smem + s * stage_bytes;
         const int k0 = (k_first + k) * 64;
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kTsThreads, 2)
         if constexpr (KIND == kTgGluFwd) {
           tma_load_3d(dst, &maps.b[0], &full[s], k0, fb * 64, 0, keep_w);
           tma_load_3d(dst + kTsWeightBytes / 2, &maps.b[0], &full[s], k0, fb * 64, 1, keep_w);
-        } else if (pr.b_mn) {
+        } else if (w_mn) {
           tma_load_2d(dst, &maps.b[0], &full[s], fb * 128, k0, keep_w);
           tma_load_2d(dst + kTsWeightBytes / 2, &maps.b[0], &full[s], fb * 128 + 64, k0, keep_w);
         } else {
@@ -193,10 +194,11 @@ __global__ void __launch_bounds__(kTsThreads, 2)
     }
   } else if (warp == 1) {
     // ================= MMA issuer =================
-    if (lane == 0) {
+    if (elect_one()) {
+      const bool w_mn = pr.b_mn;
       const uint32_t idesc = (P.f16 ? idesc_f16_f32(128, nt) : idesc_bf16_f32(128, nt)) |
-                             (pr.b_mn ? 1u << 15 : 0u);
-      const uint64_t wstep = pr.b_mn ? 2048 >> 4 : 32 >> 4;
+                             (w_mn ? 1u << 15 : 0u);
+      const uint64_t wstep = w_mn ? 2048 >> 4 : 32 >> 4;
       int s = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kTsThreads, 2)
         }
         tc_fence_after();
         const uint32_t sw = smem_u32(smem + s * stage_bytes);
-        uint64_t wd = pr.b_mn ? sdesc_mn_sw128(sw) : sdesc_k_sw128(sw);
+        uint64_t wd = w_mn ? sdesc_mn_sw128(sw) : sdesc_k_sw128(sw);
         uint64_t xd = sdesc_k_sw128(sw + kTsWeightBytes);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {

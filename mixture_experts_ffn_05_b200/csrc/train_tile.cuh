@@ -6,6 +6,18 @@
 
 namespace moe {
 
+// True in one lane of a converged warp.  The loops that issue bulk copies and MMAs run under it
+// and not under `lane == 0`: the compiler then knows that one thread is active and keeps these
+// instructions' operands in uniform registers.  Under `lane == 0` a K step took 810 cycles to
+// issue, under this 510, which is the tensor cores' own rate for a pair's 256 x 256 x 64.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Shared-memory descriptor of an MN-major tile laid out by TMA boxes of 64 (M or N) elements x
 // 64 K rows with 128-byte swizzling: a box is 8 KB, the next 64 elements follow it (leading
 // byte offset), 8 K rows are 1024 bytes apart (stride byte offset).
