@@ -82,6 +82,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Arrival that orders no memory: a released accumulator was read with tcgen05.ld and its wait,
+// while a releasing arrival would first wait for the tile's global stores (2 to 3 K cycles).
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- tiles
 struct TgTile {
   int p, m, n;
@@ -558,12 +565,21 @@ __global__ void __launch_bounds__(kTgThreads, 1)
       tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                              static_cast<uint32_t>(ab * C::kAccCols);
+      // the leader's MMA waits for all epilogue warps of both CTAs; each releases the accumulator
+      // when it has read its last chunk, before it stores it
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(cluster_addr(&acc_empty[ab], 0));
+      };
       for (int i = grp; i < chunks; i += 2) {
+        const bool last = i + 2 >= chunks;
         const Chunk c{lane, row0, pr.m, n0 + 32 * i, pr.n};
         if constexpr (KIND == kTgGluFwd) {
           float g[32], u[32];
           tmem_ld32(tbase + 32 * i, g);
           tmem_ld32(tbase + BN / 2 + 32 * i, u);
+          if (last) release();
           if (P.gu != nullptr) {
             keep(P, stage, c, 0, g);
             keep(P, stage, c, 1, u);
@@ -574,12 +590,13 @@ __global__ void __launch_bounds__(kTgThreads, 1)
           float dh[32], g[32], u[32];
           read_kept(P, stage, c, kg, g);
           read_kept(P, stage, c, ku, u);
-          if (i + 2 < chunks) {
+          if (!last) {
             const Chunk next{lane, row0, pr.m, c.col + 64, pr.n};
             kg = request_kept(P, next, 0);
             ku = request_kept(P, next, 1);
           }
           tmem_ld32(tbase + 32 * i, dh);
+          if (last) release();
           glu_backward(dh, g, u, P.silu);
           put16(stage, c, P.dgu, 2 * static_cast<int64_t>(pr.n), g, P.f16);
           put16(stage, c, static_cast<uint16_t*>(P.dgu) + pr.n, 2 * static_cast<int64_t>(pr.n), u,
@@ -588,20 +605,14 @@ __global__ void __launch_bounds__(kTgThreads, 1)
         } else {
           float v[32];
           tmem_ld32(tbase + 32 * i, v);
+          if (last) release();
           if (pr.out_f32 || pr.accumulate)
             put32(stage, c, pr.out, pr.ld_out, v, pr.out_f32, pr.accumulate, P.f16);
           else
             put16(stage, c, pr.out, pr.ld_out, v, P.f16);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (PAIR)
-          mbar_arrive_cluster(cluster_addr(&acc_empty[ab], 0));  // the leader's MMA waits
-        else
-          mbar_arrive(&acc_empty[ab]);
-      }
+      if (grp >= chunks) release();
       ab ^= 1;
       if (ab == 0) aph ^= 1u;
     }
