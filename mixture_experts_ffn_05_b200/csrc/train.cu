@@ -160,32 +160,56 @@ struct Product {
   int out_f32, accumulate;
 };
 
-// The tile shape of a launch: pairs on 256 x 256 tiles when those alone occupy the GPU, else
-// smaller tiles so that more SMs take part.
-TgShape pick_shape(const Product* pr, int n, bool glu_fwd) {
-  auto tiles = [&](TgShape s) {
-    int64_t t = 0;
-    for (int i = 0; i < n; ++i)
-      t += ceil_div(pr[i].m, tg_tile_m(s)) * ceil_div((glu_fwd ? 2 : 1) * pr[i].n, tg_tile_n(s));
-    return t;
-  };
-  if (tiles(kTgPair256) >= kB200Sms / 4) return kTgPair256;
-  if (tiles(kTgOne128) >= kB200Sms) return kTgOne128;
-  return kTgOne64;
-}
+// How a launch is tiled: by the least time that these estimates give, in SM cycles as measured
+// at 2816 x 2112, 1000 x 1352 and 512 x 384 with 8 to 8192 tokens.  A K step (64) takes 510 in a
+// CTA pair (256 x 256), about 600 in a single CTA (128 x 128) or one of a few-token tile, 450 in
+// 128 x 64; a launch costs 17 K on pairs, whose last tile's epilogue alone is 4 to 7 K, and 8 to
+// 12 K else.  A tile's epilogue overlaps the next tile's K loop but is not shorter than 3.3 K on
+// pairs.  At 2816 x 2112, 768 tokens, dh and dx take 55 us on pairs and 66 us on few-token
+// tiles; at 256 tokens the latter take 29 us and pairs 36 us.
+struct Plan {
+  bool small;    // train_small.cu; else `shape`
+  TgShape shape;
+  int splits;    // small: CTAs that share a tile
+  int64_t cycles;
+};
 
-// Few tokens: one product whose tiles of 128 features all run at one time.
-bool small_product(const Product& pr, bool glu_fwd) {
-  return !pr.a.mn && !pr.out_f32 && !pr.accumulate &&
-         ceil_div(pr.m, 128) * ceil_div(pr.n, glu_fwd ? 64 : 128) <= kTsMostCtas;
+Plan plan_products(const Product* pr, int n, bool glu_fwd) {
+  Plan best{};
+  for (TgShape s : {kTgPair256, kTgOne128, kTgOne64}) {
+    const int64_t step = s == kTgPair256 ? 510 : s == kTgOne128 ? 600 : 450;
+    const int64_t fixed = s == kTgPair256 ? 17000 : s == kTgOne128 ? 13000 : 12000;
+    const int64_t least = s == kTgPair256 ? 3300 : s == kTgOne128 ? 1700 : 1000;
+    const int64_t ctas = s == kTgPair256 ? kB200Sms / 2 : kB200Sms;
+    int64_t tiles = 0, longest = 0;
+    for (int i = 0; i < n; ++i) {
+      tiles += ceil_div(pr[i].m, tg_tile_m(s)) * ceil_div((glu_fwd ? 2 : 1) * pr[i].n, tg_tile_n(s));
+      longest = std::max(longest, std::max(ceil_div(pr[i].k, 64) * step, least));
+    }
+    const int64_t c = fixed + ceil_div(tiles, ctas) * longest;
+    if (best.cycles == 0 || c < best.cycles) best = Plan{false, s, 1, c};
+  }
+  if (n == 1 && !pr[0].a.mn && !pr[0].out_f32 && !pr[0].accumulate) {
+    const int nt = ts_tokens(pr[0].m);
+    const int64_t tiles = ceil_div(pr[0].m, nt) * ceil_div(pr[0].n, glu_fwd ? 64 : 128);
+    const int64_t k = ceil_div(pr[0].k, 64);
+    for (int splits = 1; splits <= 8 && k >= 2 * splits; splits *= 2) {
+      if (tiles * splits > ts_most_ctas(splits, nt)) break;
+      const int64_t c = 8000 + (splits > 1 ? 1000 : 0) + ceil_div(k, splits) * (nt > 64 ? 580 : 400) +
+                        nt * 20 / splits;
+      if (c < best.cycles) best = Plan{true, kTgOne128, splits, c};
+    }
+  }
+  return best;
 }
 
 moe_status_t run_products(const Product* pr, int n, TgParams p, cudaStream_t s, bool pdl) {
   const int sms = device_sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
   const bool glu_fwd = p.kind == kTgGluFwd;
-  const bool small = n == 1 && small_product(pr[0], glu_fwd);
-  const TgShape shape = small ? kTgOne128 : pick_shape(pr, n, glu_fwd);
+  const Plan plan = plan_products(pr, n, glu_fwd);
+  const bool small = plan.small;
+  const TgShape shape = plan.shape;
   const int nt = ts_tokens(pr[0].m);
   const int tm = small ? nt : tg_tile_m(shape), tn = tg_tile_n(shape);
   const int b_rows = shape == kTgPair256 ? 128 : tn;  // B rows that one CTA loads
@@ -215,7 +239,7 @@ moe_status_t run_products(const Product* pr, int n, TgParams p, cudaStream_t s, 
     maps.b[i] = maps.b[0];
   }
   p.nprob = n;
-  if (small) return cuda_status(launch_train_small(maps, p, nt, s, pdl));
+  if (small) return cuda_status(launch_train_small(maps, p, nt, plan.splits, s, pdl));
   return cuda_status(launch_train_gemm(shape, maps, p, sms, s, pdl));
 }
 
@@ -405,7 +429,7 @@ moe_status_t moe_mlp_backward(const moe_mlp_config_t* cfg, int32_t T, const moe_
   if (dx != nullptr) {
     out[n++] = Product{T, H, 2 * D, {dgu, 2 * D, false}, {w_gate_up, H, true},
                        dx->data, dx->ld, 0, 0};
-    if (small_product(out[0], false)) {  // a launch of its own, whose K loop is split
+    if (plan_products(out, 1, false).small) {  // a launch of its own, whose K loop is split
       if ((st = run_products(out, 1, mlp_params(cfg, kTgStore, nullptr, ws), s, true)) != MOE_OK)
         return st;
       n = 0;

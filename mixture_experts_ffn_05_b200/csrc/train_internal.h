@@ -99,11 +99,16 @@ cudaError_t launch_train_gemm(TgShape shape, const TgMaps& maps, const TgParams&
                               cudaStream_t s, bool pdl);
 
 // The same for few tokens (prob[0] alone): tiles of 128 features (GLU forward: 64, gate and up)
-// by nt tokens, nt a multiple of 16 up to 128, their K steps split over a cluster.  Taken while
-// its tiles fit the GPU at one time.
-constexpr int kTsMostCtas = kB200Sms;
+// by nt tokens, nt a multiple of 16 up to 128, their K steps split over a cluster of 1, 2, 4 or
+// 8 CTAs, all of them on the GPU at one time.
 constexpr int ts_tokens(int64_t T) { return T >= 128 ? 128 : static_cast<int>((T + 15) / 16 * 16); }
-cudaError_t launch_train_small(const TgMaps& maps, const TgParams& p, int nt, cudaStream_t s,
-                               bool pdl);
+// The most CTAs: above 64 tokens a CTA fills an SM, and a cluster's SMs lie in one of the GPU's
+// processor clusters, which then hold no more than 32 clusters of 4 or 14 of 8 (at 34 of 4 the
+// launch took two turns).
+constexpr int ts_most_ctas(int splits, int nt) {
+  return nt <= 64 || splits <= 2 ? kB200Sms : splits == 4 ? 128 : 112;
+}
+cudaError_t launch_train_small(const TgMaps& maps, const TgParams& p, int nt, int splits,
+                               cudaStream_t s, bool pdl);
 
 }  // namespace moe

@@ -10,8 +10,7 @@
 // four neighbouring features a lane, so that a warp writes 128 to 256 contiguous bytes.
 //
 // Weights do not depend on the kernel before: the first ring fill requests them before the
-// dependency wait, and the ring takes less than half of an SM, so that the next product's
-// weights already come in while this one runs.
+// dependency wait.
 #include "train_internal.h"
 #include "train_tile.cuh"
 
@@ -19,7 +18,10 @@ namespace moe {
 
 constexpr int kTsThreads = 320;        // producer, MMA, 8 epilogue warps
 constexpr int kTsWeightBytes = 16384;  // 128 features x 64 K elements
-constexpr int kTsRingBytes = 96 * 1024;  // two CTAs an SM
+// Ring bytes: up to 64 tokens two CTAs fit an SM, so that the next product's weights come in
+// while this one runs; above, the tokens' bytes count as much as the weights' and a deep ring
+// more (256 tokens, 2816 x 2112, forward: 23.4 us, 27.0 us with half of it).
+constexpr int ts_ring(int nt) { return (nt <= 64 ? 96 : 192) * 1024; }
 constexpr int kTsMaxStages = 8;
 
 // N tokens' sums of four neighbouring features over the cluster's CTAs; `mine` + i * `step`
@@ -332,21 +334,15 @@ __global__ void __launch_bounds__(kTsThreads, 2)
   }
 }
 
-// CTAs that share a tile: as many as the SMs hold at one time, with at least two K steps each.
-static int train_small_splits(int64_t tiles, int k_steps) {
-  int c = 1;
-  while (c < 8 && tiles * 2 * c <= kTsMostCtas && k_steps >= 4 * c) c *= 2;
-  return c;
-}
-
 template <int KIND, int SPLITS>
 static cudaError_t launch_ts(const TgMaps& maps, const TgParams& p, int nt, cudaStream_t s,
                              bool pdl) {
   const int stage = kTsWeightBytes + nt * 128;
-  const int stages = kTsRingBytes / stage < kTsMaxStages ? kTsRingBytes / stage : kTsMaxStages;
-  const int smem = 1024 + kTsRingBytes;
+  const int fit = ts_ring(nt) / stage;
+  const int stages = fit < kTsMaxStages ? fit : kTsMaxStages;
+  const int smem = 1024 + ts_ring(nt);
   auto kernel = train_small_kernel<KIND, SPLITS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + ts_ring(128));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.prob[0].m_tiles * p.prob[0].n_tiles * SPLITS));
@@ -366,10 +362,9 @@ static cudaError_t launch_ts(const TgMaps& maps, const TgParams& p, int nt, cuda
 }
 
 template <int KIND>
-static cudaError_t launch_kind(const TgMaps& maps, const TgParams& p, int nt, cudaStream_t s,
-                               bool pdl) {
-  switch (train_small_splits(static_cast<int64_t>(p.prob[0].m_tiles) * p.prob[0].n_tiles,
-                             p.prob[0].k_steps)) {
+static cudaError_t launch_kind(const TgMaps& maps, const TgParams& p, int nt, int splits,
+                               cudaStream_t s, bool pdl) {
+  switch (splits) {
     case 1: return launch_ts<KIND, 1>(maps, p, nt, s, pdl);
     case 2: return launch_ts<KIND, 2>(maps, p, nt, s, pdl);
     case 4: return launch_ts<KIND, 4>(maps, p, nt, s, pdl);
@@ -377,12 +372,12 @@ static cudaError_t launch_kind(const TgMaps& maps, const TgParams& p, int nt, cu
   }
 }
 
-cudaError_t launch_train_small(const TgMaps& maps, const TgParams& p, int nt, cudaStream_t s,
-                               bool pdl) {
+cudaError_t launch_train_small(const TgMaps& maps, const TgParams& p, int nt, int splits,
+                               cudaStream_t s, bool pdl) {
   switch (p.kind) {
-    case kTgStore: return launch_kind<kTgStore>(maps, p, nt, s, pdl);
-    case kTgGluFwd: return launch_kind<kTgGluFwd>(maps, p, nt, s, pdl);
-    case kTgGluBwd: return launch_kind<kTgGluBwd>(maps, p, nt, s, pdl);
+    case kTgStore: return launch_kind<kTgStore>(maps, p, nt, splits, s, pdl);
+    case kTgGluFwd: return launch_kind<kTgGluFwd>(maps, p, nt, splits, s, pdl);
+    case kTgGluBwd: return launch_kind<kTgGluBwd>(maps, p, nt, splits, s, pdl);
   }
   return cudaErrorInvalidValue;
 }
