@@ -109,99 +109,100 @@ def act8(rows: int, cols: int, fmt: str = "int8", parts: int = 1, device=None) -
                 parts)
 
 
-# The device's index of a tensor (-1: CPU) and a device's current stream as a handle: the calls
-# of one token take a few microseconds, of which torch.cuda.current_stream alone would be half.
+# A device's current stream as a handle, and the current device: torch.cuda.current_stream alone
+# takes longer than the rest of a call, and at one token the host's time is the call's time.
 _get_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_Tensor = torch.Tensor
 
 
-class _Call:
-    """One call's tensors: all on one device, which is current while the call is made."""
-    __slots__ = ("index", "stream")
-
-    def __init__(self, first, stream):
-        if isinstance(first, Act8):
-            first = first.codes
-        if not isinstance(first, torch.Tensor):
-            raise TypeError("an activation must be a torch.Tensor or an Act8")
-        self.index, self.stream = first.get_device(), stream
-
-    def _on_device(self, t, name):
-        if t.get_device() != self.index or self.index < 0:
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be on a CUDA device")
-            raise ValueError(f"{name} is on {t.device}, the call's first tensor on "
-                             f"{f'cuda:{self.index}' if self.index >= 0 else 'the CPU'}")
-
-    def ptr(self, t, name, dtype=None, numel=None, nullable=False):
-        if t is None:
-            if nullable:
-                return None
-            raise ValueError(f"{name} is required")
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        self._on_device(t, name)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if numel is not None and t.numel() != numel:
-            raise ValueError(f"{name} must hold {numel} elements, got {t.numel()}")
-        return t.data_ptr()
-
-    def act(self, t, name, rows, cols, dtype=None, parts=1, nullable=False):
-        """The C description of an activation [rows][parts * cols], a tensor or an Act8;
-        dtype None takes any format."""
-        if t is None:
-            if nullable:
-                return None
-            raise ValueError(f"{name} is required")
-        scales = None
-        width = parts * cols
-        if isinstance(t, Act8):
-            data = t.codes
-            if data.dtype not in (torch.int8, torch.uint8):
-                raise TypeError(f"{name}: codes must be torch.int8 or torch.uint8 (E4M3)")
-            if t.parts != parts:
-                raise ValueError(f"{name} must be a checkpoint of {parts} part(s)")
-            scales = self.ptr(t.scales, f"{name}.scales", torch.uint8,
-                              rows * parts * (-(-cols // GROUP)))
-        elif not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor or an Act8")
-        else:
-            data = t
-            if (t.dtype != dtype) if dtype is not None else (_FORMATS.get(t.dtype, 9) > F_F32):
-                raise TypeError(f"{name} must be {dtype or 'bf16, fp16 or fp32'}, got {t.dtype}")
-        self._on_device(data, name)
-        if data.shape != (rows, width):
-            raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(data.shape)}")
-        strides = data.stride()
-        if width > 1 and strides[1] != 1:
-            raise ValueError(f"{name} must have contiguous rows")
-        # of one row the stride says nothing
-        return CAct(data.data_ptr(), scales, strides[0] if rows > 1 else width,
-                    _FORMATS[data.dtype])
-
-    def run(self, name, *args):
-        fn = getattr(_fns or _lib(), name)
-        index = self.index
-        s = _raw_stream(index) if self.stream is None else self.stream.cuda_stream
-        if index == _get_device():
-            st = fn(*args, s)
-        else:
-            with torch.cuda.device(index):
-                st = fn(*args, s)
-        if st:
-            _check(name, st)
-
-
-def _shape(t, name):
-    t = t.codes if isinstance(t, Act8) else t
-    if not isinstance(t, torch.Tensor):
+def _first(t, name):
+    """(device index, rows, columns) of a call's first tensor, whose device the others share."""
+    if isinstance(t, Act8):
+        t = t.codes
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor or an Act8")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(shape)}")
+    return t.get_device(), shape[0], shape[1]
+
+
+def _wrong_device(t, name, index):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    raise ValueError(f"{name} is on {t.device}, the call's first tensor on cuda:{index}")
+
+
+def _ptr(t, name, index, dtype, numel):
+    """The address of a contiguous tensor of `numel` elements (None: any number)."""
+    if not isinstance(t, _Tensor):
+        if t is None:
+            raise ValueError(f"{name} is required")
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != index:
+        _wrong_device(t, name, index)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _act(t, name, index, rows, cols, dtype, parts=1):
+    """The C description of an activation [rows][parts * cols]: a tensor of `dtype` (None: bf16,
+    fp16 or fp32) or an Act8."""
+    width = parts * cols
+    scales = None
+    if isinstance(t, _Tensor):
+        fmt = _FORMATS.get(t.dtype, 9)
+        if (fmt > F_F32) if dtype is None else (t.dtype is not dtype):
+            raise TypeError(f"{name} must be {dtype or 'bf16, fp16 or fp32'}, got {t.dtype}")
+    elif isinstance(t, Act8):
+        if t.parts != parts:
+            raise ValueError(f"{name} must be a checkpoint of {parts} part(s)")
+        scales = _ptr(t.scales, f"{name}.scales", index, torch.uint8,
+                      rows * parts * (-(-cols // GROUP)))
+        t = t.codes
+        fmt = _FORMATS.get(t.dtype, 9)
+        if fmt != F_INT8 and fmt != F_E4M3:
+            raise TypeError(f"{name}: codes must be torch.int8 or torch.uint8 (E4M3)")
+    elif t is None:
+        raise ValueError(f"{name} is required")
+    else:
+        raise TypeError(f"{name} must be a torch.Tensor or an Act8")
+    if t.get_device() != index:
+        _wrong_device(t, name, index)
+    if t.shape != (rows, width):
+        raise ValueError(f"{name} must be [{rows}, {width}], got {tuple(t.shape)}")
+    ld, inner = t.stride()
+    if inner != 1 and width > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    # of one row the stride says nothing
+    return CAct(t.data_ptr(), scales, ld if rows > 1 else width, fmt)
+
+
+def _plain(t, name):
+    """A value that must not be an Act8."""
+    if isinstance(t, Act8):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t
+
+
+def _run(name, index, stream, *args):
+    if index < 0:
+        raise ValueError(f"{name}: the tensors must be on a CUDA device")
+    fn = getattr(_fns or _lib(), name)
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == _get_device():
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, s)
+    if st:
+        _check(name, st)
 
 
 def _zeros(n, fn, device):
@@ -212,24 +213,25 @@ def _zeros(n, fn, device):
 
 # ------------------------------------------------------------------ 8-bit checkpoints
 
-def moe_act_encode(x, kept: Act8, stream=None) -> None:
-    """Write the 8-bit checkpoint of x [rows][cols] (bf16, fp16 or fp32)."""
-    rows, cols = _shape(x, "x")
+def _checkpoint(kept):
     if not isinstance(kept, Act8):
         raise TypeError("kept must be an Act8")
-    c = _Call(x, stream)
-    c.run("moe_act_encode", rows, cols, c.act(x, "x", rows, cols),
-          c.act(kept, "kept", rows, cols))
+    return kept
+
+
+def moe_act_encode(x, kept: Act8, stream=None) -> None:
+    """Write the 8-bit checkpoint of x [rows][cols] (bf16, fp16 or fp32)."""
+    i, rows, cols = _first(_plain(x, "x"), "x")
+    _run("moe_act_encode", i, stream, rows, cols, _act(x, "x", i, rows, cols, None),
+         _act(_checkpoint(kept), "kept", i, rows, cols, None))
 
 
 def moe_act_decode(kept: Act8, out, stream=None) -> None:
     """Read an 8-bit checkpoint back into out [rows][cols] (bf16, fp16 or fp32)."""
-    rows, cols = _shape(out, "out")
-    if not isinstance(kept, Act8):
-        raise TypeError("kept must be an Act8")
-    c = _Call(out, stream)
-    c.run("moe_act_decode", rows, cols, c.act(kept, "kept", rows, cols),
-          c.act(out, "out", rows, cols))
+    i, rows, cols = _first(_plain(out, "out"), "out")
+    _run("moe_act_decode", i, stream, rows, cols,
+         _act(_checkpoint(kept), "kept", i, rows, cols, None),
+         _act(out, "out", i, rows, cols, None))
 
 
 # ------------------------------------------------------------------ norms
@@ -261,32 +263,29 @@ def moe_norm_forward(cfg, x, gain, bias, y, mean, rstd, kept: Act8 | None = None
                      stream=None) -> None:
     """y = norm(x) * gain + bias with the row statistics the backward pass needs (mean: layer
     norm only), and on request the 8-bit checkpoint of x.  gain and bias may be None."""
-    T, n = _shape(x, "x")
-    c = _Call(x, stream)
-    if kept is not None and not isinstance(kept, Act8):
-        raise TypeError("kept must be an Act8")
-    f32 = torch.float32
-    c.run("moe_norm_forward", cfg._c, T, c.act(x, "x", T, cfg.cols, cfg.dtype),
-          c.ptr(gain, "gain", cfg.param_dtype, cfg.cols, True),
-          c.ptr(bias, "bias", cfg.param_dtype, cfg.cols, True),
-          c.act(y, "y", T, cfg.cols, cfg.dtype), c.ptr(mean, "mean", f32, T, True),
-          c.ptr(rstd, "rstd", f32, T), c.act(kept, "kept", T, cfg.cols, nullable=True))
+    i, T, _ = _first(_plain(x, "x"), "x")
+    n, dt, pt, f32 = cfg.cols, cfg.dtype, cfg.param_dtype, torch.float32
+    _run("moe_norm_forward", i, stream, cfg._c, T, _act(x, "x", i, T, n, dt),
+         None if gain is None else _ptr(gain, "gain", i, pt, n),
+         None if bias is None else _ptr(bias, "bias", i, pt, n),
+         _act(_plain(y, "y"), "y", i, T, n, dt),
+         None if mean is None else _ptr(mean, "mean", i, f32, T), _ptr(rstd, "rstd", i, f32, T),
+         None if kept is None else _act(_checkpoint(kept), "kept", i, T, n, None))
 
 
 def moe_norm_backward(cfg, x, gain, mean, rstd, dy, dx, d_gain, d_bias, ws,
                       accumulate: bool = False, stream=None) -> None:
     """dx and the fp32 gradients of gain and bias (either may be None), from x or its 8-bit
     checkpoint and the forward pass's statistics.  accumulate adds to d_gain and d_bias."""
-    T, n = _shape(x, "x")
-    c = _Call(x, stream)
-    f32 = torch.float32
-    c.run("moe_norm_backward", cfg._c, T, c.act(x, "x", T, cfg.cols, cfg.dtype),
-          c.ptr(gain, "gain", cfg.param_dtype, cfg.cols, True),
-          c.ptr(mean, "mean", f32, T, True), c.ptr(rstd, "rstd", f32, T),
-          c.act(dy, "dy", T, cfg.cols, cfg.dtype), c.act(dx, "dx", T, cfg.cols, cfg.dtype),
-          c.ptr(d_gain, "d_gain", f32, cfg.cols, True),
-          c.ptr(d_bias, "d_bias", f32, cfg.cols, True), int(bool(accumulate)),
-          c.ptr(ws, "ws", torch.uint8), ws.numel())
+    i, T, _ = _first(x, "x")
+    n, dt, f32 = cfg.cols, cfg.dtype, torch.float32
+    _run("moe_norm_backward", i, stream, cfg._c, T, _act(x, "x", i, T, n, dt),
+         None if gain is None else _ptr(gain, "gain", i, cfg.param_dtype, n),
+         None if mean is None else _ptr(mean, "mean", i, f32, T), _ptr(rstd, "rstd", i, f32, T),
+         _act(_plain(dy, "dy"), "dy", i, T, n, dt), _act(_plain(dx, "dx"), "dx", i, T, n, dt),
+         None if d_gain is None else _ptr(d_gain, "d_gain", i, f32, n),
+         None if d_bias is None else _ptr(d_bias, "d_bias", i, f32, n), 1 if accumulate else 0,
+         _ptr(ws, "ws", i, torch.uint8, None), ws.numel())
 
 
 # ------------------------------------------------------------------ the gated MLP
@@ -315,14 +314,13 @@ def mlp_workspace(cfg: MlpConfig, T: int, device=None) -> torch.Tensor:
 def moe_mlp_forward(cfg, x, w_gate_up, w_down, y, ws, kept_gu=None, stream=None) -> None:
     """y = (act(x Wg^T) * (x Wu^T)) Wd^T.  kept_gu: None, or what the backward pass needs of
     it, a [T][2D] tensor or an Act8 of two parts."""
-    T, n = _shape(x, "x")
-    H, D = cfg.hidden, cfg.inter
-    c = _Call(x, stream)
-    c.run("moe_mlp_forward", cfg._c, T, c.act(x, "x", T, H, cfg.dtype),
-          c.ptr(w_gate_up, "w_gate_up", cfg.dtype, 2 * D * H),
-          c.ptr(w_down, "w_down", cfg.dtype, D * H), c.act(y, "y", T, H, cfg.dtype),
-          c.act(kept_gu, "kept_gu", T, D, cfg.dtype, 2, True), c.ptr(ws, "ws", torch.uint8),
-          ws.numel())
+    i, T, _ = _first(_plain(x, "x"), "x")
+    H, D, dt = cfg.hidden, cfg.inter, cfg.dtype
+    _run("moe_mlp_forward", i, stream, cfg._c, T, _act(x, "x", i, T, H, dt),
+         _ptr(w_gate_up, "w_gate_up", i, dt, 2 * D * H), _ptr(w_down, "w_down", i, dt, D * H),
+         _act(_plain(y, "y"), "y", i, T, H, dt),
+         None if kept_gu is None else _act(kept_gu, "kept_gu", i, T, D, dt, 2),
+         _ptr(ws, "ws", i, torch.uint8, None), ws.numel())
 
 
 def moe_mlp_backward(cfg, x, gu, w_gate_up, w_down, dy, dx, dw_gate_up, dw_down, ws,
@@ -330,18 +328,18 @@ def moe_mlp_backward(cfg, x, gu, w_gate_up, w_down, dy, dx, dw_gate_up, dw_down,
     """The gradients of x and the weights from x and gu as kept (tensors or Act8).  dx,
     dw_gate_up and dw_down may be None; the weight gradients are in cfg's dtype or fp32, both
     the same, and accumulate adds to what they hold."""
-    T, n = _shape(dy, "dy")
-    H, D = cfg.hidden, cfg.inter
-    c = _Call(dy, stream)
-    grad = next((g.dtype for g in (dw_gate_up, dw_down) if g is not None), cfg.dtype)
-    if grad not in (cfg.dtype, torch.float32):
-        raise TypeError(f"weight gradients must be {cfg.dtype} or torch.float32, got {grad}")
-    c.run("moe_mlp_backward", cfg._c, T,
-          c.act(x, "x", T, H, cfg.dtype, nullable=dw_gate_up is None),
-          c.act(gu, "gu", T, D, cfg.dtype, 2),
-          c.ptr(w_gate_up, "w_gate_up", cfg.dtype, 2 * D * H, dx is None),
-          c.ptr(w_down, "w_down", cfg.dtype, D * H),
-          c.act(dy, "dy", T, H, cfg.dtype), c.act(dx, "dx", T, H, cfg.dtype, nullable=True),
-          c.ptr(dw_gate_up, "dw_gate_up", grad, 2 * D * H, True),
-          c.ptr(dw_down, "dw_down", grad, D * H, True), _FORMATS[grad], int(bool(accumulate)),
-          c.ptr(ws, "ws", torch.uint8), ws.numel())
+    i, T, _ = _first(_plain(dy, "dy"), "dy")
+    H, D, dt = cfg.hidden, cfg.inter, cfg.dtype
+    grad = next((g.dtype for g in (dw_gate_up, dw_down) if g is not None), dt)
+    if grad not in (dt, torch.float32):
+        raise TypeError(f"weight gradients must be {dt} or torch.float32, got {grad}")
+    _run("moe_mlp_backward", i, stream, cfg._c, T,
+         None if x is None and dw_gate_up is None else _act(x, "x", i, T, H, dt),
+         _act(gu, "gu", i, T, D, dt, 2),
+         None if w_gate_up is None and dx is None else
+         _ptr(w_gate_up, "w_gate_up", i, dt, 2 * D * H),
+         _ptr(w_down, "w_down", i, dt, D * H), _act(dy, "dy", i, T, H, dt),
+         None if dx is None else _act(_plain(dx, "dx"), "dx", i, T, H, dt),
+         None if dw_gate_up is None else _ptr(dw_gate_up, "dw_gate_up", i, grad, 2 * D * H),
+         None if dw_down is None else _ptr(dw_down, "dw_down", i, grad, D * H), _FORMATS[grad],
+         1 if accumulate else 0, _ptr(ws, "ws", i, torch.uint8, None), ws.numel())
