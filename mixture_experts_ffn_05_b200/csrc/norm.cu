@@ -14,11 +14,12 @@
 // what makes W (8 NV + 9) smallest: 2816 columns take 4 warps of 24 elements.
 //
 // Wide form (columns, strides and bases that 16-byte accesses fit): a thread owns units of 16
-// bytes of the activation's format, U = 8 or 4 columns, unit u at column U (t + 32 W u); it
-// reads back only the units that it copied itself, so the ring needs no barrier.  Narrow form
-// (any other): the row is copied as the aligned 16-byte chunks that cover it, and element j is
-// column t + 32 W j, so that a warp's accesses stay contiguous.  In both a group of 32 columns
-// lies within one warp, where the checkpoint's scale is formed.
+// bytes of the activation's format, U = 8 or 4 columns; it reads back only the units that it
+// copied itself, so the ring needs no barrier.  Narrow form (any other): the row is copied as
+// the aligned 16-byte chunks that cover it, and U is 1.  In both warp w's unit u of lane l is at
+// column 256 NV w + 32 U u + U l: accesses are contiguous over a warp, differ by constants from
+// unit to unit, and a group of 32 columns lies within one warp, where the checkpoint's scale
+// is formed.
 //
 // The gradients of gain and bias are sums over all rows: a thread owns its columns for the
 // whole kernel and adds its rows in registers, the teams of a CTA meet in shared memory, each
@@ -134,6 +135,12 @@ struct Rows {
   }
 };
 
+__device__ __forceinline__ float sum_of(uint64_t p) {
+  float a, b;
+  of_pair(p, a, b);
+  return a + b;
+}
+
 template <int FMT, int NV, bool WIDE>
 struct NormThread {
   static constexpr int E = 8 * NV;              // elements a thread
@@ -141,6 +148,7 @@ struct NormThread {
   static constexpr int U = WIDE ? 16 / ES : 1;  // columns of a unit
   static constexpr int NU = E / U;
   int t, tpr, warps, wt, lane, team, cols;
+  int c0, room;  // the thread's first column, columns from there
   float* red;  // the team's two buffers of a warp's sums
   int turn;
 
@@ -152,11 +160,14 @@ struct NormThread {
     wt = t >> 5;
     lane = t & 31;
     cols = n;
+    c0 = wt * 32 * E + U * lane;
+    room = n - c0;
     red = buf + team * w * 2;  // one warp a row: unused
     turn = 0;
   }
-  __device__ __forceinline__ int unit(int u) const { return U * (t + u * tpr); }
-  __device__ __forceinline__ int col(int j) const { return unit(j / U) + j % U; }
+  __device__ __forceinline__ static constexpr int off(int u) { return 32 * U * u; }
+  __device__ __forceinline__ bool in(int u) const { return off(u) < room; }
+  __device__ __forceinline__ int col(int j) const { return c0 + off(j / U) + j % U; }
 
   __device__ __forceinline__ void sync() const {
     if (warps == 1)
@@ -207,35 +218,50 @@ struct NormThread {
       if (col(j) < cols) dst[place(col(j), cols)] = f[j];
   }
   __device__ __forceinline__ void param(float (&f)[U], const float* p, int u) const {
-    const int c = unit(u);
 #pragma unroll
     for (int e = 0; e < U; ++e) f[e] = 0.f;
-    if (c >= cols) return;
+    if (!in(u)) return;
     if constexpr (U == 1) {
-      f[0] = p[c];
+      f[0] = p[c0 + off(u)];
     } else {
 #pragma unroll
       for (int k = 0; k < U / 4; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(p + place(c + 4 * k, cols));
+        const float4 v = *reinterpret_cast<const float4*>(
+            p + place(c0 + 4 * k, cols) + off(u) * 4 / U);
         f[4 * k] = v.x; f[4 * k + 1] = v.y; f[4 * k + 2] = v.z; f[4 * k + 3] = v.w;
       }
     }
   }
 
-  __device__ __forceinline__ void store(void* row, const float (&f)[E]) const {
+  // The parameters of UP elements: a unit's, or in the narrow form two units'.
+  static constexpr int UP = U == 1 ? 2 : U;
+  __device__ __forceinline__ void params(float (&f)[UP], const float* p, int u) const {
+    if constexpr (U == 1) {
+      float a[1], b[1];
+      param(a, p, 2 * u);
+      param(b, p, 2 * u + 1);
+      f[0] = a[0];
+      f[1] = b[0];
+    } else {
+      param(f, p, u);
+    }
+  }
+
+  __device__ __forceinline__ void store(uint8_t* row, const float (&f)[E]) const {
+    row += c0 * ES;
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      if (unit(u) >= cols) continue;
+      if (!in(u)) continue;
       if constexpr (!WIDE) {
-        store1<FMT>(row, unit(u), f[u]);
+        store1<FMT>(row, off(u), f[u]);
       } else if constexpr (FMT == kFmtF32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(row) + unit(u)) =
+        *reinterpret_cast<float4*>(row + off(u) * ES) =
             make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
       } else {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = f[8 * u + e];
-        store8<FMT>(row, unit(u), v);
+        store8<FMT>(row, off(u), v);
       }
     }
   }
@@ -245,9 +271,11 @@ struct NormThread {
   __device__ __forceinline__ void request(uint8_t* slot, const uint8_t* src) const {
     constexpr int XS = fmt_bytes(XF);
     if constexpr (WIDE) {
+      slot += c0 * XS;
+      src += c0 * XS;
 #pragma unroll
       for (int u = 0; u < NU; ++u)
-        if (unit(u) < cols) cp_async<U * XS>(slot + unit(u) * XS, src + unit(u) * XS);
+        if (in(u)) cp_async<U * XS>(slot + off(u) * XS, src + off(u) * XS);
     } else {
       const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15);
       const int end = shift + cols * XS;  // nothing behind the row is read
@@ -263,16 +291,16 @@ struct NormThread {
     constexpr int XS = fmt_bytes(XF);
     constexpr bool I8 = XF == kFmtInt8;
     if constexpr (!WIDE) slot += reinterpret_cast<uintptr_t>(src) & 15;
+    slot += c0 * XS;
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const bool in = unit(u) < cols;
       float scale = 0.f;
       if constexpr (XS == 1)
-        scale = scale_value(__shfl_sync(0xffffffffu, byte, WIDE ? u * U + lane * U / 32 : u));
+        scale = scale_value(__shfl_sync(0xffffffffu, byte, u * U + lane * U / 32));
 #pragma unroll
       for (int e = 0; e < U; ++e) f[U * u + e] = 0.f;
-      if (!in) continue;
-      const uint8_t* at = slot + unit(u) * XS;
+      if (!in(u)) continue;
+      const uint8_t* at = slot + off(u) * XS;
       if constexpr (!WIDE) {
         if constexpr (XS == 1)
           f[u] = decode1<I8>(*at, scale);
@@ -298,7 +326,7 @@ struct NormThread {
 
   // Lane l's scale byte: the l-th of the E groups that this warp's columns form.
   __device__ __forceinline__ int scale_bytes(const uint8_t* row) const {
-    const int g = WIDE ? U * (wt + lane / U * warps) + lane % U : wt + lane * warps;
+    const int g = wt * E + lane;
     return lane < E && g * kGroup8 < cols ? row[g] : 1;
   }
 
@@ -306,9 +334,10 @@ struct NormThread {
   template <bool INT8>
   __device__ __forceinline__ void keep(const float (&f)[E], uint8_t* codes,
                                        uint8_t* scales) const {
+    codes += c0;
+    scales += c0 / kGroup8;
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const int c = unit(u);
       float own[U];
 #pragma unroll
       for (int e = 0; e < U; ++e) own[e] = f[U * u + e];
@@ -319,12 +348,12 @@ struct NormThread {
       } else {
         m = __reduce_max_sync(0xffffffffu, m);
       }
-      if (c >= cols) continue;
+      if (!in(u)) continue;
       const int sb = scale_byte<INT8>(m);
       const float inv = scale_inverse(sb);
-      if (c % kGroup8 == 0) scales[c / kGroup8] = static_cast<uint8_t>(sb);
+      if (U * lane % kGroup8 == 0) scales[U * u] = static_cast<uint8_t>(sb);
       if constexpr (!WIDE) {
-        codes[c] = static_cast<uint8_t>(encode1<INT8>(f[u], inv));
+        codes[off(u)] = static_cast<uint8_t>(encode1<INT8>(f[u], inv));
       } else {
         uint32_t w[U / 4];
 #pragma unroll
@@ -333,9 +362,9 @@ struct NormThread {
           w[k] = encode4<INT8>(v[0], v[1], v[2], v[3], inv);
         }
         if constexpr (U == 8)
-          *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2*>(codes + off(u)) = make_uint2(w[0], w[1]);
         else
-          *reinterpret_cast<uint32_t*>(codes + c) = w[0];
+          *reinterpret_cast<uint32_t*>(codes + off(u)) = w[0];
       }
     }
   }
@@ -346,7 +375,7 @@ template <int FMT, int NV, bool WIDE, bool LAYER>
 __global__ void __launch_bounds__(norm_forward_threads(NV), 1)
     norm_forward_kernel(NormArgs a, int warps, int teams, int stages) {
   using Th = NormThread<FMT, NV, WIDE>;
-  constexpr int E = Th::E, U = Th::U;
+  constexpr int E = Th::E, U = Th::U, UP = Th::UP;
   __shared__ float red[2 * kNormRed];
   extern __shared__ uint4 ring4[];
   Th th(warps, a.cols, red);
@@ -374,21 +403,36 @@ __global__ void __launch_bounds__(norm_forward_threads(NV), 1)
   if (LAYER) th.fill(bias, a.bias, a.pfmt, 0.f);
   __syncthreads();
   for (int s = 0; rows > 0; --rows, row += step) {
-    float x[E], mean[1] = {0.f}, var[1] = {0.f};
+    float x[E], mean[1] = {0.f}, var[1];
     cp_async_wait_all_but(stages - 1);
     if (!WIDE) th.sync();  // the others' chunks
     th.template read<FMT>(x, ring + s * slot, now.take(), 0);
     if (LAYER) {
+      uint64_t m2 = 0;
 #pragma unroll
-      for (int j = 0; j < E; ++j) mean[0] += x[j];
+      for (int j = 0; j < E; j += 2) m2 = add2(m2, pair_of(x[j], x[j + 1]));
+      mean[0] = sum_of(m2);
       th.sum(mean);
       mean[0] *= inv_n;
     }
+    const uint64_t less = pair_of(-mean[0], -mean[0]);
+    uint64_t v2 = 0;
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float d = LAYER ? (th.col(j) < a.cols ? x[j] - mean[0] : 0.f) : x[j];
-      var[0] = fmaf(d, d, var[0]);
+    for (int j = 0; j < E; j += 2) {
+      uint64_t d = pair_of(x[j], x[j + 1]);
+      if (LAYER) {  // columns past the end add nothing
+        d = add2(d, less);
+        if (U == 1) {
+          float d0, d1;
+          of_pair(d, d0, d1);
+          d = pair_of(th.in(j) ? d0 : 0.f, th.in(j + 1) ? d1 : 0.f);
+        } else if (!th.in(j / U)) {
+          d = 0;
+        }
+      }
+      v2 = fma2(d, d, v2);
     }
+    var[0] = sum_of(v2);
     th.sum(var);
     if (!WIDE && warps == 1) th.sync();
     request(s);  // every thread of the team holds its part of the row
@@ -404,16 +448,20 @@ __global__ void __launch_bounds__(norm_forward_threads(NV), 1)
       else
         th.template keep<false>(x, codes.take(), scales.take());
     }
+    const uint64_t rstd2 = pair_of(rstd, rstd);
 #pragma unroll
-    for (int u = 0; u < Th::NU; ++u) {
-      float g[U], b[U];
-      th.param(g, gain, u);
-      if (LAYER) th.param(b, bias, u);
+    for (int u = 0; u < E / UP; ++u) {
+      float g[UP], b[UP];
+      th.params(g, gain, u);
+      if (LAYER) th.params(b, bias, u);
 #pragma unroll
-      for (int e = 0; e < U; ++e) {
-        float& v = x[U * u + e];
-        const float z = (LAYER ? v - mean[0] : v) * rstd;
-        v = LAYER ? fmaf(z, g[e], b[e]) : z * g[e];
+      for (int e = 0; e < UP; e += 2) {
+        float *v = x + UP * u + e;
+        uint64_t z = pair_of(v[0], v[1]);
+        if (LAYER) z = add2(z, less);
+        z = mul2(z, rstd2);
+        const uint64_t g2 = pair_of(g[e], g[e + 1]);
+        of_pair(LAYER ? fma2(z, g2, pair_of(b[e], b[e + 1])) : mul2(z, g2), v[0], v[1]);
       }
     }
     th.store(out.take(), x);
@@ -428,7 +476,7 @@ __global__ void __launch_bounds__(norm_backward_threads(NV, LAYER), 1)
     norm_backward_kernel(NormArgs a, int warps, int teams, int stages) {
   using Th = NormThread<FMT, NV, WIDE>;
   constexpr bool X8 = fmt_bytes(XF) == 1;
-  constexpr int E = Th::E, U = Th::U;
+  constexpr int E = Th::E, U = Th::U, UP = Th::UP;
   __shared__ float red[2 * kNormRed];
   extern __shared__ uint4 ring4[];  // gain, ring; at the end gain, the teams' sums [teams][cols]
   pdl_trigger();
@@ -477,36 +525,50 @@ __global__ void __launch_bounds__(norm_backward_threads(NV, LAYER), 1)
     const int byte = byte_n;
     small();
     float z[E], d[E];  // z, and dy then a = dy gain
-    float sums[LAYER ? 2 : 1] = {};
+    float sums[LAYER ? 2 : 1];
     cp_async_wait_all_but(stages - 1);
     if (!WIDE) th.sync();
     th.template read<XF>(z, ring + s * slot, now_x.take(), byte);
     th.template read<FMT>(d, ring + s * slot + slot_x, now_dy.take(), 0);
     // sums of a z and (layer) of a, and this thread's share of the parameter gradients;
     // columns past the end have dy = 0 and add nothing
+    const uint64_t less = pair_of(-mean, -mean), rstd2 = pair_of(rstd, rstd);
+    uint64_t az = 0, as = 0;
 #pragma unroll
-    for (int u = 0; u < Th::NU; ++u) {
-      float g[U];
-      th.param(g, gain, u);
+    for (int u = 0; u < E / UP; ++u) {
+      float g[UP];
+      th.params(g, gain, u);
 #pragma unroll
-      for (int e = 0; e < U; ++e) {
-        const int j = U * u + e;
-        z[j] = LAYER ? (z[j] - mean) * rstd : z[j] * rstd;
-        if (LAYER) db[j] += d[j];
-        dg[j] = fmaf(d[j], z[j], dg[j]);
-        d[j] *= g[e];
-        sums[0] = fmaf(d[j], z[j], sums[0]);
-        if (LAYER) sums[LAYER] += d[j];
+      for (int e = 0; e < UP; e += 2) {
+        const int j = UP * u + e;
+        uint64_t zz = pair_of(z[j], z[j + 1]), dd = pair_of(d[j], d[j + 1]);
+        if (LAYER) {
+          zz = add2(zz, less);
+          of_pair(add2(pair_of(db[j], db[j + 1]), dd), db[j], db[j + 1]);
+        }
+        zz = mul2(zz, rstd2);
+        of_pair(fma2(dd, zz, pair_of(dg[j], dg[j + 1])), dg[j], dg[j + 1]);
+        dd = mul2(dd, pair_of(g[e], g[e + 1]));
+        az = fma2(dd, zz, az);
+        if (LAYER) as = add2(as, dd);
+        of_pair(zz, z[j], z[j + 1]);
+        of_pair(dd, d[j], d[j + 1]);
       }
     }
+    sums[0] = sum_of(az);
+    if (LAYER) sums[LAYER] = sum_of(as);
     th.sum(sums);
     if (!WIDE && warps == 1) th.sync();
     request(s);
     if (++s == stages) s = 0;
-    const float c1 = sums[0] * inv_n, c2 = LAYER ? sums[LAYER] * inv_n : 0.f;
+    // dx = rstd (a - mean(a)) - z rstd mean(a z)
+    const float c1 = -rstd * (sums[0] * inv_n), c2 = LAYER ? -rstd * (sums[LAYER] * inv_n) : 0.f;
 #pragma unroll
-    for (int j = 0; j < E; ++j)
-      d[j] = rstd * fmaf(-z[j], c1, LAYER ? d[j] - c2 : d[j]);
+    for (int j = 0; j < E; j += 2) {
+      uint64_t dd = pair_of(d[j], d[j + 1]);
+      dd = LAYER ? fma2(dd, rstd2, pair_of(c2, c2)) : mul2(dd, rstd2);
+      of_pair(fma2(pair_of(z[j], z[j + 1]), pair_of(c1, c1), dd), d[j], d[j + 1]);
+    }
     th.store(out.take(), d);
   }
   cp_async_wait<0>();
