@@ -156,11 +156,12 @@ __device__ __forceinline__ void put16(uint4* stage, const Chunk& c, void* base, 
   for (int i = 0; i < 4; ++i) stage[stage16(c.lane, i)] = pack16(v + 8 * i, f16);
   __syncwarp();
   uint16_t* out = static_cast<uint16_t*>(base) + static_cast<int64_t>(c.row0) * ld + c.col;
+  uint4 w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = stage[stage16(c.row(k), c.piece())];
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    if (c.in(k))
-      *reinterpret_cast<uint4*>(out + c.row(k) * ld + 8 * c.piece()) =
-          stage[stage16(c.row(k), c.piece())];
+    if (c.in(k)) *reinterpret_cast<uint4*>(out + c.row(k) * ld + 8 * c.piece()) = w[k];
   __syncwarp();
 }
 
