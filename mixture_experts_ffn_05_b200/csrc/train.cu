@@ -160,34 +160,44 @@ struct Product {
   int out_f32, accumulate;
 };
 
-// How a launch is tiled: by the least time that these estimates give, in SM cycles as measured
-// at 2816 x 2112, 1000 x 1352 and 512 x 384 with 8 to 8192 tokens.  A K step (64) takes 510 in a
-// CTA pair (256 x 256), about 600 in a single CTA (128 x 128) or one of a few-token tile, 450 in
-// 128 x 64; a launch costs 17 K on pairs, whose last tile's epilogue alone is 4 to 7 K, and 8 to
-// 12 K else.  A tile's epilogue overlaps the next tile's K loop but is not shorter than 3.3 K on
-// pairs.  At 2816 x 2112, 768 tokens, dh and dx take 55 us on pairs and 66 us on few-token
-// tiles; at 256 tokens the latter take 29 us and pairs 36 us.
+// How a launch is tiled: by the least time that these estimates give, in ns, fitted to launches
+// of every form at 2816 x 2112, 2048 x 1024, 1000 x 1352 and 512 x 384 with 4 to 4096 tokens.
+// A tile's time is its K steps or its epilogue, whichever is longer, and the last epilogue is
+// not overlapped; tiles of 256 x 256 on CTA pairs move the fewest bytes a FLOP but leave most
+// SMs idle when they are few.  At 2816 x 2112 (k = 44 steps) the gate_up product of 1001
+// tokens takes 23.8 us on pairs, 26.2 on 128 x 128 and 36.7 on 128 x 64; of 512 tokens 22.4,
+// 15.5 and 21.4; of 256 tokens 21.5, 14.7 and 13.2; of 64 tokens 12.4 on 128 x 64 and 9.3 on
+// few-token tiles split 4 ways.  Rows of 1000 elements, whose pieces of 128 bytes lie in two
+// lines, shift that: of 4096 tokens 32.7, 42.9 and 56.4 (1000 x 1352, k = 16).
+struct TileCost {
+  int step, step_off;   // a K step of 64; with rows that start off a 128-byte line
+  int fixed, fixed_bwd; // launch, setup, last epilogue; that of dh
+  int least;            // a tile's epilogue
+};
+constexpr TileCost kTileCost[3] = {{320, 515, 8000, 14500, 2200}, {222, 480, 4500, 7500, 2400},
+                                   {180, 326, 4200, 5600, 1360}};
+
 struct Plan {
-  bool small;    // train_small.cu; else `shape`
+  bool small;  // train_small.cu; else `shape`
   TgShape shape;
-  int splits;    // small: CTAs that share a tile
-  int64_t cycles;
+  int splits;  // small: CTAs that share a tile
+  int64_t ns;
 };
 
-Plan plan_products(const Product* pr, int n, bool glu_fwd) {
+Plan plan_products(const Product* pr, int n, int kind) {
+  const bool glu_fwd = kind == kTgGluFwd, glu_bwd = kind == kTgGluBwd;
   Plan best{};
   for (TgShape s : {kTgPair256, kTgOne128, kTgOne64}) {
-    const int64_t step = s == kTgPair256 ? 510 : s == kTgOne128 ? 600 : 450;
-    const int64_t fixed = s == kTgPair256 ? 17000 : s == kTgOne128 ? 13000 : 12000;
-    const int64_t least = s == kTgPair256 ? 3300 : s == kTgOne128 ? 1700 : 1000;
+    const TileCost& tc = kTileCost[s];
     const int64_t ctas = s == kTgPair256 ? kB200Sms / 2 : kB200Sms;
-    int64_t tiles = 0, longest = 0;
+    int64_t tiles = 0, longest = tc.least;
     for (int i = 0; i < n; ++i) {
+      const bool off = pr[i].a.ld % 64 != 0 || pr[i].b.ld % 64 != 0;
       tiles += ceil_div(pr[i].m, tg_tile_m(s)) * ceil_div((glu_fwd ? 2 : 1) * pr[i].n, tg_tile_n(s));
-      longest = std::max(longest, std::max(ceil_div(pr[i].k, 64) * step, least));
+      longest = std::max(longest, ceil_div(pr[i].k, 64) * (off ? tc.step_off : tc.step));
     }
-    const int64_t c = fixed + ceil_div(tiles, ctas) * longest;
-    if (best.cycles == 0 || c < best.cycles) best = Plan{false, s, 1, c};
+    const int64_t ns = (glu_bwd ? tc.fixed_bwd : tc.fixed) + ceil_div(tiles, ctas) * longest;
+    if (best.ns == 0 || ns < best.ns) best = Plan{false, s, 1, ns};
   }
   if (n == 1 && !pr[0].a.mn && !pr[0].out_f32 && !pr[0].accumulate) {
     const int nt = ts_tokens(pr[0].m);
@@ -195,9 +205,9 @@ Plan plan_products(const Product* pr, int n, bool glu_fwd) {
     const int64_t k = ceil_div(pr[0].k, 64);
     for (int splits = 1; splits <= 8 && k >= 2 * splits; splits *= 2) {
       if (tiles * splits > ts_most_ctas(splits, nt)) break;
-      const int64_t c = 8000 + (splits > 1 ? 1000 : 0) + ceil_div(k, splits) * (nt > 64 ? 580 : 400) +
-                        nt * 20 / splits;
-      if (c < best.cycles) best = Plan{true, kTgOne128, splits, c};
+      const int64_t ns = 5000 + 8 * nt + ceil_div(k, splits) * (180 + nt * 6 / 10) +
+                         nt * (glu_bwd ? 80 : 25) / splits;
+      if (ns < best.ns) best = Plan{true, kTgOne128, splits, ns};
     }
   }
   return best;
@@ -207,7 +217,7 @@ moe_status_t run_products(const Product* pr, int n, TgParams p, cudaStream_t s, 
   const int sms = device_sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
   const bool glu_fwd = p.kind == kTgGluFwd;
-  const Plan plan = plan_products(pr, n, glu_fwd);
+  const Plan plan = plan_products(pr, n, p.kind);
   const bool small = plan.small;
   const TgShape shape = plan.shape;
   const int nt = ts_tokens(pr[0].m);
@@ -429,7 +439,7 @@ moe_status_t moe_mlp_backward(const moe_mlp_config_t* cfg, int32_t T, const moe_
   if (dx != nullptr) {
     out[n++] = Product{T, H, 2 * D, {dgu, 2 * D, false}, {w_gate_up, H, true},
                        dx->data, dx->ld, 0, 0};
-    if (plan_products(out, 1, false).small) {  // a launch of its own, whose K loop is split
+    if (plan_products(out, 1, kTgStore).small) {  // a launch of its own, whose K loop is split
       if ((st = run_products(out, 1, mlp_params(cfg, kTgStore, nullptr, ws), s, true)) != MOE_OK)
         return st;
       n = 0;
