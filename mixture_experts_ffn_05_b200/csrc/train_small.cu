@@ -21,7 +21,15 @@ constexpr int kTsWeightBytes = 16384;  // 128 features x 64 K elements
 // Ring bytes: up to 64 tokens two CTAs fit an SM, so that the next product's weights come in
 // while this one runs; above, the tokens' bytes count as much as the weights' and a deep ring
 // more (256 tokens, 2816 x 2112, forward: 23.4 us, 27.0 us with half of it).
-constexpr int ts_ring(int nt) { return (nt <= 64 ? 96 : 192) * 1024; }
+constexpr int ts_ring(int nt) { return (nt <= 64 ? 108 : 192) * 1024; }
+
+// The cluster barrier in two parts, for a thread at a time.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 constexpr int kTsMaxStages = 8;
 
 // N tokens' sums of four neighbouring features over the cluster's CTAs; `mine` + i * `step`
@@ -257,8 +265,13 @@ __global__ void __launch_bounds__(kTsThreads, 2)
     }
   }
   __syncwarp();
-  cluster_sync();  // all CTAs' sums are in place
+  cluster_sync();  // all CTAs' sums are in place, and tensor memory is read
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, cols);
+  }
 
+  bool arrived = false;
   if (warp >= 2 && !abort_flag) {
     const int f0 = KIND == kTgGluFwd ? fb * 64 + 4 * (lane & 15) : fb * 128 + 4 * lane;
     const int tokens = min(nt, pr.m - tb * nt);
@@ -280,6 +293,10 @@ __global__ void __launch_bounds__(kTsThreads, 2)
       }
       cluster_sums<SPLITS>(v, reinterpret_cast<const float*>(smem) + t0 * 128 + 4 * lane,
                            step * 128, count, rank);
+      if (t0 + kBatch * step >= tokens) {  // the last reads of the peers' sums
+        cluster_arrive();  // before the stores, which a release after them would wait for
+        arrived = true;
+      }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         if (i >= count) break;
@@ -324,14 +341,9 @@ __global__ void __launch_bounds__(kTsThreads, 2)
       }
     }
   }
-  // ---- teardown: no CTA exits while its peers may still read its sums
-  __syncwarp();
-  tc_fence_before();
-  cluster_sync();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem_base, cols);
-  }
+  // ---- no CTA exits while its peers may still read its sums
+  if (!arrived) cluster_arrive();
+  cluster_wait();
 }
 
 template <int KIND, int SPLITS>
