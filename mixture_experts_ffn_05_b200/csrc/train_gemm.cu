@@ -132,42 +132,35 @@ struct Chunk {
   __device__ __forceinline__ bool in(int k) const {
     return row0 + row(k) < m && col + 8 * piece() < n;
   }
+  // of access 0, in elements; each next one is 8 rows on
+  __device__ __forceinline__ int64_t first(int64_t ld) const {
+    return static_cast<int64_t>(row0 + (lane >> 2)) * ld + col + 8 * piece();
+  }
 };
 
-__device__ __forceinline__ uint4 pack16(const float* v, bool f16) {
-  return f16 ? make_uint4(pack2_f16(v[0], v[1]), pack2_f16(v[2], v[3]), pack2_f16(v[4], v[5]),
-                          pack2_f16(v[6], v[7]))
-             : make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-}
-__device__ __forceinline__ void unpack16(const uint4& u, float* v, bool f16) {
-  float t[8];
-  if (f16)
-    unpack8_f16(u, t);
-  else
-    unpack8(u, t);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = t[e];
-}
-
 // base: the output's column 0; ld elements.
+template <bool F16>
 __device__ __forceinline__ void put16(uint4* stage, const Chunk& c, void* base, int64_t ld,
-                                      const float (&v)[32], bool f16) {
+                                      const float (&v)[32]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) stage[stage16(c.lane, i)] = pack16(v + 8 * i, f16);
+  for (int i = 0; i < 4; ++i) stage[stage16(c.lane, i)] = pack16<F16>(v + 8 * i);
   __syncwarp();
-  uint16_t* out = static_cast<uint16_t*>(base) + static_cast<int64_t>(c.row0) * ld + c.col;
+  uint16_t* out = static_cast<uint16_t*>(base) + c.first(ld);
   uint4 w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) w[k] = stage[stage16(c.row(k), c.piece())];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (c.in(k)) *reinterpret_cast<uint4*>(out + c.row(k) * ld + 8 * c.piece()) = w[k];
+  for (int k = 0; k < 4; ++k) {
+    if (c.in(k)) *reinterpret_cast<uint4*>(out) = w[k];
+    out += 8 * ld;
+  }
   __syncwarp();
 }
 
 // fp32 outputs, and sums to 16- or 32-bit ones (rounded once).
+template <bool F16>
 __device__ __forceinline__ void put32(uint4* stage, const Chunk& c, void* base, int64_t ld,
-                                      const float (&v)[32], bool f32, bool add, bool f16) {
+                                      const float (&v)[32], bool f32, bool add) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     *reinterpret_cast<float4*>(stage + stage32(c.lane, i)) =
@@ -191,10 +184,9 @@ __device__ __forceinline__ void put32(uint4* stage, const Chunk& c, void* base, 
       uint2* o = reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at);
       const uint2 old = *o;
       float t[8];
-      unpack16(make_uint4(old.x, old.y, 0u, 0u), t, f16);
+      unpack16<F16>(make_uint4(old.x, old.y, 0u, 0u), t);
       w.x += t[0]; w.y += t[1]; w.z += t[2]; w.w += t[3];
-      *o = f16 ? make_uint2(pack2_f16(w.x, w.y), pack2_f16(w.z, w.w))
-               : make_uint2(pack2(w.x, w.y), pack2(w.z, w.w));
+      *o = make_uint2(pack_two<F16>(w.x, w.y), pack_two<F16>(w.z, w.w));
     }
   }
   __syncwarp();
@@ -218,15 +210,18 @@ __device__ __forceinline__ void keep8(const TgParams& P, uint4* stage4, const Ch
                                            encode4<INT8>(f[4], f[5], f[6], f[7], inv));
   }
   __syncwarp();
-  uint8_t* out = static_cast<uint8_t*>(P.gu) + static_cast<int64_t>(c.row0) * P.ld_gu +
-                 static_cast<int64_t>(half) * c.n + c.col;
+  uint8_t* out = static_cast<uint8_t*>(P.gu) + c.first(P.ld_gu) + static_cast<int64_t>(half) * c.n;
+  uint2 w[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (c.in(k))
-      *reinterpret_cast<uint2*>(out + c.row(k) * P.ld_gu + 8 * c.piece()) =
-          stage[stage16(c.row(k), c.piece())];
+  for (int k = 0; k < 4; ++k) w[k] = stage[stage16(c.row(k), c.piece())];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (c.in(k)) *reinterpret_cast<uint2*>(out) = w[k];
+    out += 8 * P.ld_gu;
+  }
   __syncwarp();
 }
+template <bool F16>
 __device__ __forceinline__ void keep(const TgParams& P, uint4* stage, const Chunk& c, int half,
                                      const float (&v)[32]) {
   if (P.gu_fmt == kFmtInt8)
@@ -234,8 +229,7 @@ __device__ __forceinline__ void keep(const TgParams& P, uint4* stage, const Chun
   else if (P.gu_fmt == kFmtE4m3)
     keep8<false>(P, stage, c, half, v);
   else
-    put16(stage, c, static_cast<uint16_t*>(P.gu) + static_cast<int64_t>(half) * c.n, P.ld_gu, v,
-          P.f16);
+    put16<F16>(stage, c, static_cast<uint16_t*>(P.gu) + static_cast<int64_t>(half) * c.n, P.ld_gu, v);
 }
 
 // The same read back: requested (early, into registers) and turned into rows.
@@ -245,31 +239,31 @@ struct Kept {
 };
 __device__ __forceinline__ Kept request_kept(const TgParams& P, const Chunk& c, int half) {
   Kept r;
-  const int64_t at = static_cast<int64_t>(c.row0) * P.ld_gu + static_cast<int64_t>(half) * c.n +
-                     c.col + 8 * c.piece();
-  const bool eight = fmt_bytes(P.gu_fmt) == 1;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    r.p[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (!c.in(k)) continue;
-    if (eight) {
-      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(P.gu) + at +
-                                                      c.row(k) * P.ld_gu);
-      r.p[k].x = w.x;
-      r.p[k].y = w.y;
-    } else {
-      r.p[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.gu) + at +
-                                               c.row(k) * P.ld_gu);
-    }
-  }
+  const int64_t at = c.first(P.ld_gu) + static_cast<int64_t>(half) * c.n, step = 8 * P.ld_gu;
   r.scale = 1;
-  if (eight && c.row0 + c.lane < c.m) {
+  if (fmt_bytes(P.gu_fmt) == 1) {
+    const uint8_t* p = static_cast<const uint8_t*>(P.gu) + at;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint2 w = c.in(k) ? *reinterpret_cast<const uint2*>(p) : make_uint2(0u, 0u);
+      r.p[k] = make_uint4(w.x, w.y, 0u, 0u);
+      p += step;
+    }
     const int groups = (c.n + kGroup8 - 1) / kGroup8;
-    r.scale = P.gu_scales[(static_cast<int64_t>(c.row0 + c.lane) * 2 + half) * groups +
-                          c.col / kGroup8];
+    if (c.row0 + c.lane < c.m)
+      r.scale = P.gu_scales[(static_cast<int64_t>(c.row0 + c.lane) * 2 + half) * groups +
+                            c.col / kGroup8];
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(P.gu) + at;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      r.p[k] = c.in(k) ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
+      p += step;
+    }
   }
   return r;
 }
+template <bool F16>
 __device__ __forceinline__ void read_kept(const TgParams& P, uint4* stage, const Chunk& c,
                                           const Kept& r, float (&v)[32]) {
 #pragma unroll
@@ -281,7 +275,7 @@ __device__ __forceinline__ void read_kept(const TgParams& P, uint4* stage, const
   __syncwarp();
   if (fmt_bytes(P.gu_fmt) != 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unpack16(w[i], v + 8 * i, P.f16);
+    for (int i = 0; i < 4; ++i) unpack16<F16>(w[i], v + 8 * i);
     return;
   }
   const float s = scale_value(r.scale);
@@ -301,19 +295,20 @@ __device__ __forceinline__ void read_kept(const TgParams& P, uint4* stage, const
 }
 
 // h = act(g) u, over g.
-__device__ __forceinline__ void glu_forward(float (&g)[32], const float (&u)[32], bool silu) {
+template <bool SILU>
+__device__ __forceinline__ void glu_forward(float (&g)[32], const float (&u)[32]) {
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
-    const Gate2 ga = gate_of<false>(pair_of(g[e], g[e + 1]), silu);
+    const Gate2 ga = gate_of<false, SILU>(pair_of(g[e], g[e + 1]));
     of_pair(mul2(ga.a, pair_of(u[e], u[e + 1])), g[e], g[e + 1]);
   }
 }
 // dg, du and h over g, u and dh.
-__device__ __forceinline__ void glu_backward(float (&dh)[32], float (&g)[32], float (&u)[32],
-                                             bool silu) {
+template <bool SILU>
+__device__ __forceinline__ void glu_backward(float (&dh)[32], float (&g)[32], float (&u)[32]) {
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
-    const Gate2 ga = gate_of<true>(pair_of(g[e], g[e + 1]), silu);
+    const Gate2 ga = gate_of<true, SILU>(pair_of(g[e], g[e + 1]));
     const uint64_t d = pair_of(dh[e], dh[e + 1]), uu = pair_of(u[e], u[e + 1]);
     of_pair(mul2(mul2(d, uu), ga.da), g[e], g[e + 1]);
     of_pair(mul2(d, ga.a), u[e], u[e + 1]);
@@ -322,7 +317,7 @@ __device__ __forceinline__ void glu_backward(float (&dh)[32], float (&g)[32], fl
 }
 
 // ---------------------------------------------------------------- the kernel
-template <bool PAIR, int BN, int KIND>
+template <bool PAIR, int BN, int KIND, bool F16>
 __global__ void __launch_bounds__(kTgThreads, 1)
     train_gemm_kernel(const __grid_constant__ TgMaps maps, const __grid_constant__ TgParams P) {
   using C = TgCfg<PAIR, BN>;
@@ -467,7 +462,7 @@ __global__ void __launch_bounds__(kTgThreads, 1)
         const TgProblem& pr = P.prob[tl.p];
         const int k_steps = pr.k_steps;
         const bool a_mn = pr.a_mn, b_mn = pr.b_mn;
-        const uint32_t idesc = (P.f16 ? idesc_f16_f32(C::kTileM, BN) : idesc_bf16_f32(C::kTileM, BN)) |
+        const uint32_t idesc = (F16 ? idesc_f16_f32(C::kTileM, BN) : idesc_bf16_f32(C::kTileM, BN)) |
                                (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
         // 16 K elements: 32 bytes along a K-major row, 16 rows of 128 bytes MN-major
         const uint64_t astep = a_mn ? 2048 >> 4 : 32 >> 4;
@@ -582,15 +577,18 @@ __global__ void __launch_bounds__(kTgThreads, 1)
           tmem_ld32(tbase + BN / 2 + 32 * i, u);
           if (last) release();
           if (P.gu != nullptr) {
-            keep(P, stage, c, 0, g);
-            keep(P, stage, c, 1, u);
+            keep<F16>(P, stage, c, 0, g);
+            keep<F16>(P, stage, c, 1, u);
           }
-          glu_forward(g, u, P.silu);
-          put16(stage, c, pr.out, pr.ld_out, g, P.f16);
+          if (P.silu)
+            glu_forward<true>(g, u);
+          else
+            glu_forward<false>(g, u);
+          put16<F16>(stage, c, pr.out, pr.ld_out, g);
         } else if constexpr (KIND == kTgGluBwd) {
           float dh[32], g[32], u[32];
-          read_kept(P, stage, c, kg, g);
-          read_kept(P, stage, c, ku, u);
+          read_kept<F16>(P, stage, c, kg, g);
+          read_kept<F16>(P, stage, c, ku, u);
           if (!last) {
             const Chunk next{lane, row0, pr.m, c.col + 64, pr.n};
             kg = request_kept(P, next, 0);
@@ -598,19 +596,22 @@ __global__ void __launch_bounds__(kTgThreads, 1)
           }
           tmem_ld32(tbase + 32 * i, dh);
           if (last) release();
-          glu_backward(dh, g, u, P.silu);
-          put16(stage, c, P.dgu, 2 * static_cast<int64_t>(pr.n), g, P.f16);
-          put16(stage, c, static_cast<uint16_t*>(P.dgu) + pr.n, 2 * static_cast<int64_t>(pr.n), u,
-                P.f16);
-          if (pr.out != nullptr) put16(stage, c, pr.out, pr.ld_out, dh, P.f16);
+          if (P.silu)
+            glu_backward<true>(dh, g, u);
+          else
+            glu_backward<false>(dh, g, u);
+          const int64_t ld = 2 * static_cast<int64_t>(pr.n);
+          put16<F16>(stage, c, P.dgu, ld, g);
+          put16<F16>(stage, c, static_cast<uint16_t*>(P.dgu) + pr.n, ld, u);
+          if (pr.out != nullptr) put16<F16>(stage, c, pr.out, pr.ld_out, dh);
         } else {
           float v[32];
           tmem_ld32(tbase + 32 * i, v);
           if (last) release();
           if (pr.out_f32 || pr.accumulate)
-            put32(stage, c, pr.out, pr.ld_out, v, pr.out_f32, pr.accumulate, P.f16);
+            put32<F16>(stage, c, pr.out, pr.ld_out, v, pr.out_f32, pr.accumulate);
           else
-            put16(stage, c, pr.out, pr.ld_out, v, P.f16);
+            put16<F16>(stage, c, pr.out, pr.ld_out, v);
         }
       }
       if (grp >= chunks) release();
@@ -633,11 +634,11 @@ __global__ void __launch_bounds__(kTgThreads, 1)
   }
 }
 
-template <bool PAIR, int BN, int KIND>
+template <bool PAIR, int BN, int KIND, bool F16>
 static cudaError_t launch_tg(const TgMaps& maps, const TgParams& p, int sms, cudaStream_t s,
                              bool pdl) {
   using C = TgCfg<PAIR, BN>;
-  auto kernel = train_gemm_kernel<PAIR, BN, KIND>;
+  auto kernel = train_gemm_kernel<PAIR, BN, KIND, F16>;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
@@ -664,15 +665,22 @@ static cudaError_t launch_tg(const TgMaps& maps, const TgParams& p, int sms, cud
   return cudaLaunchKernelEx(&cfg, kernel, maps, p);
 }
 
+template <int KIND, bool F16>
+static cudaError_t launch_shape(TgShape shape, const TgMaps& maps, const TgParams& p, int sms,
+                               cudaStream_t s, bool pdl) {
+  switch (shape) {
+    case kTgPair256: return launch_tg<true, 256, KIND, F16>(maps, p, sms, s, pdl);
+    case kTgOne128: return launch_tg<false, 128, KIND, F16>(maps, p, sms, s, pdl);
+    case kTgOne64: return launch_tg<false, 64, KIND, F16>(maps, p, sms, s, pdl);
+  }
+  return cudaErrorInvalidValue;
+}
+
 template <int KIND>
 static cudaError_t launch_kind(TgShape shape, const TgMaps& maps, const TgParams& p, int sms,
                                cudaStream_t s, bool pdl) {
-  switch (shape) {
-    case kTgPair256: return launch_tg<true, 256, KIND>(maps, p, sms, s, pdl);
-    case kTgOne128: return launch_tg<false, 128, KIND>(maps, p, sms, s, pdl);
-    case kTgOne64: return launch_tg<false, 64, KIND>(maps, p, sms, s, pdl);
-  }
-  return cudaErrorInvalidValue;
+  return p.f16 ? launch_shape<KIND, true>(shape, maps, p, sms, s, pdl)
+               : launch_shape<KIND, false>(shape, maps, p, sms, s, pdl);
 }
 
 cudaError_t launch_train_gemm(TgShape shape, const TgMaps& maps, const TgParams& p, int sms,

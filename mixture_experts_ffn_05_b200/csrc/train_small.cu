@@ -71,6 +71,10 @@ __device__ __forceinline__ void put4(void* base, int64_t i, const float (&v)[4],
           : make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
 }
 
+__device__ __forceinline__ uint64_t gate_act(uint64_t g, bool silu) {
+  return silu ? gate_of<false, true>(g).a : gate_of<false, false>(g).a;
+}
+
 // A group of 32 features is eight lanes' four values; every lane takes part.
 template <bool INT8>
 __device__ __forceinline__ void keep4(const TgParams& P, const float (&v)[4], int64_t row, int half,
@@ -316,7 +320,7 @@ __global__ void __launch_bounds__(kTsThreads, 2)
           for (int e = 0; e < 4; ++e) up[e] = __shfl_xor_sync(0xffffffffu, v[i][e], 16);
 #pragma unroll
           for (int e = 0; e < 4; e += 2)
-            of_pair(mul2(gate_of<false>(pair_of(v[i][e], v[i][e + 1]), P.silu).a,
+            of_pair(mul2(gate_act(pair_of(v[i][e], v[i][e + 1]), P.silu),
                          pair_of(up[e], up[e + 1])),
                     h[e], h[e + 1]);
           if (live && half == 0) put4(pr.out, row * pr.ld_out + f0, h, P.f16);
@@ -324,7 +328,8 @@ __global__ void __launch_bounds__(kTsThreads, 2)
           if constexpr (KIND == kTgGluBwd) {
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-              const Gate2 ga = gate_of<true>(pair_of(g[i][e], g[i][e + 1]), P.silu);
+              const uint64_t gg = pair_of(g[i][e], g[i][e + 1]);
+              const Gate2 ga = P.silu ? gate_of<true, true>(gg) : gate_of<true, false>(gg);
               const uint64_t d = pair_of(v[i][e], v[i][e + 1]), uu = pair_of(u[i][e], u[i][e + 1]);
               of_pair(mul2(mul2(d, uu), ga.da), g[i][e], g[i][e + 1]);
               of_pair(mul2(d, ga.a), u[i][e], u[i][e + 1]);

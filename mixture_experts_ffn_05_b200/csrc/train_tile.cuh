@@ -37,6 +37,28 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// Eight values in 16 bits.  The format is a template parameter: as a run-time choice both
+// conversions would be computed for every value.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_two(float a, float b) {
+  return F16 ? pack2_f16(a, b) : pack2(a, b);
+}
+template <bool F16>
+__device__ __forceinline__ uint4 pack16(const float* v) {
+  return make_uint4(pack_two<F16>(v[0], v[1]), pack_two<F16>(v[2], v[3]),
+                    pack_two<F16>(v[4], v[5]), pack_two<F16>(v[6], v[7]));
+}
+template <bool F16>
+__device__ __forceinline__ void unpack16(const uint4& u, float* v) {
+  float t[8];
+  if (F16)
+    unpack8_f16(u, t);
+  else
+    unpack8(u, t);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = t[e];
+}
+
 // ---------------------------------------------------------------- the activation
 // Both are a = g L(z) with the logistic L(z) = 1 / (1 + exp(-z)): z = g (silu) or
 // 2 sqrt(2/pi) (g + 0.044715 g^3) (gelu_tanh, since (1 + tanh w) / 2 = L(2w)).  Then
@@ -46,12 +68,12 @@ __device__ __forceinline__ uint64_t both(float v) { return pair_of(v, v); }
 struct Gate2 {
   uint64_t a, da;
 };
-template <bool WITH_D>
-__device__ __forceinline__ Gate2 gate_of(uint64_t g, bool silu) {
+template <bool WITH_D, bool SILU>
+__device__ __forceinline__ Gate2 gate_of(uint64_t g) {
   constexpr float kLog2e = 1.4426950408889634f, kC0 = 1.5957691216057308f, kC1 = 0.044715f;
   const uint64_t g2 = mul2(g, g);
-  uint64_t w = mul2(g, both(silu ? -kLog2e : -kC0 * kLog2e));  // exp(-z) = 2^w
-  if (!silu) w = mul2(w, fma2(g2, both(kC1), both(1.f)));
+  uint64_t w = mul2(g, both(SILU ? -kLog2e : -kC0 * kLog2e));  // exp(-z) = 2^w
+  if (!SILU) w = mul2(w, fma2(g2, both(kC1), both(1.f)));
   float w0, w1, l0, l1;
   of_pair(w, w0, w1);
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w0) : "f"(w0));
@@ -65,7 +87,7 @@ __device__ __forceinline__ Gate2 gate_of(uint64_t g, bool silu) {
   r.da = 0;
   if (WITH_D) {
     uint64_t t = mul2(r.a, fma2(l, both(-1.f), both(1.f)));
-    if (!silu) {
+    if (!SILU) {
       float q0, q1;
       of_pair(g2, q0, q1);
       t = mul2(t, fma2(pair_of(fminf(q0, 256.f), fminf(q1, 256.f)), both(3.f * kC1 * kC0), both(kC0)));
