@@ -42,7 +42,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if all(os.path.getmtime(d) <= t for d in deps):
             return LIB
     tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "--threads", "0", "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
            "-I" + os.path.join(ROOT, "include"), "-o", tmp, *srcs]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

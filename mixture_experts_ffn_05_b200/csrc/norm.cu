@@ -37,7 +37,7 @@ constexpr int kNormRed = 2 * 768 / 32;         // floats of a round of sums: two
 
 // Threads of a CTA: as many as the registers of 8 NV elements allow without spills (which, the
 // ring leaving little of L1, would go to L2).  NV = 4 only serves rows of more than 12288
-// columns, and spills in backward.
+// columns (layer norm's backward: 9216), and spills in backward.
 __host__ __device__ constexpr int norm_forward_threads(int nv) {
   return nv <= 2 ? 768 : nv == 3 ? 640 : 512;
 }
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(norm_backward_threads(NV, LAYER), 1)
     norm_backward_kernel(NormArgs a, int warps, int teams, int stages) {
   using Th = NormThread<FMT, NV, WIDE>;
   constexpr bool X8 = fmt_bytes(XF) == 1;
-  constexpr int E = Th::E, U = Th::U, UP = Th::UP;
+  constexpr int E = Th::E, UP = Th::UP;
   __shared__ float red[2 * kNormRed];
   extern __shared__ uint4 ring4[];  // gain, ring; at the end gain, the teams' sums [teams][cols]
   pdl_trigger();
