@@ -95,15 +95,19 @@ moe_status_t check_mlp(const moe_mlp_config_t* c, int32_t T) {
 
 struct MlpLayout {
   size_t h, dgu, x16, total;  // after the status word
+  int64_t ld_h, ld_dgu, ld_x; // rows start on 128-byte lines, as the copies like them best
 };
 
 MlpLayout mlp_layout(const moe_mlp_config_t* c, int32_t T) {
   const size_t t = static_cast<size_t>(T), H = c->hidden, D = c->inter;
   MlpLayout L;
+  L.ld_h = static_cast<int64_t>((D + 63) / 64 * 64);
+  L.ld_dgu = static_cast<int64_t>((2 * D + 63) / 64 * 64);
+  L.ld_x = static_cast<int64_t>((H + 63) / 64 * 64);
   L.h = kAlign;
-  L.dgu = L.h + align_up(t * D * 2);
-  L.x16 = L.dgu + align_up(t * 2 * D * 2);
-  L.total = L.x16 + align_up(t * H * 2);
+  L.dgu = L.h + align_up(t * L.ld_h * 2);
+  L.x16 = L.dgu + align_up(t * L.ld_dgu * 2);
+  L.total = L.x16 + align_up(t * L.ld_x * 2);
   return L;
 }
 
@@ -383,10 +387,10 @@ moe_status_t moe_mlp_forward(const moe_mlp_config_t* cfg, int32_t T, const moe_a
   if (!ws_ok(ws, ws_bytes, L.total)) return MOE_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* h = at<void>(ws, L.h);
-  const Product up{T, D, H, {x->data, x->ld, false}, {w_gate_up, H, false}, h, D, 0, 0};
+  const Product up{T, D, H, {x->data, x->ld, false}, {w_gate_up, H, false}, h, L.ld_h, 0, 0};
   if ((st = run_products(&up, 1, mlp_params(cfg, kTgGluFwd, kept_gu, ws), s, false)) != MOE_OK)
     return st;
-  const Product down{T, H, D, {h, D, false}, {w_down, D, false}, y->data, y->ld, 0, 0};
+  const Product down{T, H, D, {h, L.ld_h, false}, {w_down, D, false}, y->data, y->ld, 0, 0};
   return run_products(&down, 1, mlp_params(cfg, kTgStore, nullptr, ws), s, true);
 }
 
@@ -424,20 +428,21 @@ moe_status_t moe_mlp_backward(const moe_mlp_config_t* cfg, int32_t T, const moe_
   const void* x16 = x != nullptr ? x->data : nullptr;
   int64_t ldx = x != nullptr ? x->ld : 0;
   if (dw_gate_up != nullptr && eight_bits(x->format)) {  // exact in bf16: operands as they were kept
-    const moe_act_t wide{at<void>(ws, L.x16), nullptr, H, cfg->format};
+    const moe_act_t wide{at<void>(ws, L.x16), nullptr, L.ld_x, cfg->format};
     if ((st = act8_call(T, cfg->hidden, &wide, x, false, stream)) != MOE_OK) return st;
     x16 = wide.data;
-    ldx = H;
+    ldx = L.ld_x;
   }
   TgParams p = mlp_params(cfg, kTgGluBwd, gu, ws);
   p.dgu = dgu;
+  p.ld_dgu = L.ld_dgu;
   const Product dh{T, D, H, {dy->data, dy->ld, false}, {w_down, D, true},
-                   dw_down != nullptr ? h : nullptr, D, 0, 0};
+                   dw_down != nullptr ? h : nullptr, L.ld_h, 0, 0};
   if ((st = run_products(&dh, 1, p, s, false)) != MOE_OK) return st;
   Product out[3];
   int n = 0;
   if (dx != nullptr) {
-    out[n++] = Product{T, H, 2 * D, {dgu, 2 * D, false}, {w_gate_up, H, true},
+    out[n++] = Product{T, H, 2 * D, {dgu, L.ld_dgu, false}, {w_gate_up, H, true},
                        dx->data, dx->ld, 0, 0};
     if (plan_products(out, 1, kTgStore).small) {  // a launch of its own, whose K loop is split
       if ((st = run_products(out, 1, mlp_params(cfg, kTgStore, nullptr, ws), s, true)) != MOE_OK)
@@ -446,9 +451,9 @@ moe_status_t moe_mlp_backward(const moe_mlp_config_t* cfg, int32_t T, const moe_
     }
   }
   if (dw_gate_up != nullptr)
-    out[n++] = Product{2 * D, H, T, {dgu, 2 * D, true}, {x16, ldx, true}, dw_gate_up, H, f32, acc};
+    out[n++] = Product{2 * D, H, T, {dgu, L.ld_dgu, true}, {x16, ldx, true}, dw_gate_up, H, f32, acc};
   if (dw_down != nullptr)
-    out[n++] = Product{H, D, T, {dy->data, dy->ld, true}, {h, D, true}, dw_down, D, f32, acc};
+    out[n++] = Product{H, D, T, {dy->data, dy->ld, true}, {h, L.ld_h, true}, dw_down, D, f32, acc};
   if (n == 0) return MOE_OK;
   return run_products(out, n, mlp_params(cfg, kTgStore, nullptr, ws), s, true);
 }

@@ -600,9 +600,8 @@ __global__ void __launch_bounds__(kTgThreads, 1)
             glu_backward<true>(dh, g, u);
           else
             glu_backward<false>(dh, g, u);
-          const int64_t ld = 2 * static_cast<int64_t>(pr.n);
-          put16<F16>(stage, c, P.dgu, ld, g);
-          put16<F16>(stage, c, static_cast<uint16_t*>(P.dgu) + pr.n, ld, u);
+          put16<F16>(stage, c, P.dgu, P.ld_dgu, g);
+          put16<F16>(stage, c, static_cast<uint16_t*>(P.dgu) + pr.n, P.ld_dgu, u);
           if (pr.out != nullptr) put16<F16>(stage, c, pr.out, pr.ld_out, dh);
         } else {
           float v[32];

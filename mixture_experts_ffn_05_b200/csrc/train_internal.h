@@ -83,6 +83,7 @@ struct TgParams {
   int64_t ld_gu;
   int gu_fmt;
   void* dgu;          // kTgGluBwd: [m][2n] in 16 bits
+  int64_t ld_dgu;
   unsigned* status;
   uint64_t timeout_ns;
 };

@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kTsThreads, 2)
               of_pair(mul2(d, ga.a), u[i][e], u[i][e + 1]);
               of_pair(mul2(ga.a, uu), v[i][e], v[i][e + 1]);
             }
-            const int64_t at = row * 2 * pr.n + f0;
+            const int64_t at = row * P.ld_dgu + f0;
             put4(P.dgu, at, g[i], P.f16);
             put4(P.dgu, at + pr.n, u[i], P.f16);
             if (pr.out != nullptr) put4(pr.out, row * pr.ld_out + f0, v[i], P.f16);
