@@ -638,8 +638,10 @@ int norm_backward_max_ctas(int T) { return T < kB200Sms ? T : kB200Sms; }
 template <typename K>
 static cudaError_t norm_launch(K kernel, const NormShape& sh, const NormArgs& a, cudaStream_t s) {
   if (sh.smem > 40 * 1024) {
+    // the limit belongs to the kernel and not to this call: always the same, so that a call
+    // on another host thread cannot lower it between here and the launch
     const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sh.smem));
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem);
     if (e != cudaSuccess) return e;
   }
   return launch_k(kernel, dim3(sh.grid), dim3(32 * sh.warps * sh.teams), sh.smem, s, false, a,
@@ -685,6 +687,7 @@ static cudaError_t backward_shape(const NormArgs& a, cudaStream_t s) {
                             norm_param(a.cols),
                             [](int nv) { return norm_backward_threads(nv, LAYER); });
   if (sh.teams > 1) {  // the teams' sums at the end
+    // (two rows a team fit, and a row is at least 3 bytes a column: so do these 4)
     const size_t sums = norm_param(a.cols) + static_cast<size_t>(sh.teams) * a.cols * sizeof(float);
     if (sums > sh.smem) sh.smem = sums;
   }

@@ -1,0 +1,65 @@
+"""Calls from several host threads at once, each with tensors, workspaces and a stream of its own."""
+import threading
+
+import pytest
+import torch
+
+from mixture_experts_ffn_05_b200 import train
+from tests.test_gpu_train_norm import Case as NormCase
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    train._lib()
+
+
+def norm_calls(c, stream):
+    """A norm's two calls as ready arguments of the library's functions, so that threads spend
+    their time in the library, where the interpreter's lock does not part them."""
+    l, n, dt = train._lib(), c.n, c.x.dtype
+
+    def act(t):
+        return train._act(t, "t", t.get_device(), c.T, n, dt)
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+
+    s = stream.cuda_stream
+    return ((l.moe_norm_forward, (c.cfg.c(), c.T, act(c.x), ptr(c.gain), ptr(c.bias), act(c.y),
+                                  ptr(c.mean), ptr(c.rstd), None, s)),
+            (l.moe_norm_backward, (c.cfg.c(), c.T, act(c.x), ptr(c.gain), ptr(c.mean),
+                                   ptr(c.rstd), act(c.dy), act(c.dx), ptr(c.d_gain),
+                                   ptr(c.d_bias), 0, ptr(c.ws), c.ws.numel(), s)))
+
+
+@pytest.mark.parametrize("which", [0, 1], ids=["forward", "backward"])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norms_of_few_and_many_rows(kind, which):
+    """The same kernel with little shared memory (few rows: two teams a CTA) and with much of it
+    (many rows): no call may lower the limit that another one is about to launch with."""
+    cases = [NormCase(T, 2816, kind, seed=T + i).run() for i, T in enumerate((296, 3000) * 2)]
+    outs = lambda c: (c.y, c.dx, c.d_gain, c.rstd)  # noqa: E731
+    want = [[t.clone() for t in outs(c)] for c in cases]
+    torch.cuda.synchronize()
+    start, refused = threading.Barrier(len(cases)), []
+
+    def work(c, stream):
+        fn, args = norm_calls(c, stream)[which]
+        start.wait()
+        refused.append(sum(fn(*args) != 0 for _ in range(4000)))
+
+    streams = [torch.cuda.Stream() for _ in cases]
+    threads = [threading.Thread(target=work, args=a) for a in zip(cases, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert refused == [0] * len(cases)
+    for c, w in zip(cases, want):
+        for t, f in zip(outs(c), w):
+            assert torch.equal(t, f)
