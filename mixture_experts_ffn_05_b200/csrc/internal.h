@@ -8,8 +8,8 @@
 
 namespace moe {
 
-// The driver's tensor-map encoder (looked up once; NULL without a driver) and the current
-// device's SM count (0 on failure).
+// The driver's tensor-map encoder (looked up once; NULL without a driver), with a context
+// current on the calling thread, and the current device's SM count (0 on failure).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 int device_sm_count();
 

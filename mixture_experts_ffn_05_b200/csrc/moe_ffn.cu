@@ -281,6 +281,7 @@ T* at(void* ws, size_t off) {
 // ---------------------------------------------------------------- devices and TMA
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+PFN_cuCtxGetCurrent_v4000 g_ctx_current = nullptr;
 std::once_flag g_encode_once;
 int g_sm_count[64] = {0};
 
@@ -290,13 +291,24 @@ namespace moe {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
+    void *fn = nullptr, *ctx = nullptr;
+    cudaDriverEntryPointQueryResult q, qc;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) ==
             cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
+        cudaGetDriverEntryPoint("cuCtxGetCurrent", &ctx, cudaEnableDefault, &qc) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess && qc == cudaDriverEntryPointSuccess) {
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+      g_ctx_current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(ctx);
+    }
   });
+  if (g_encode == nullptr) return nullptr;
+  // The encoder wants a context current on its thread.  A host thread that has made no
+  // runtime call yet has none: give it the current device's, as the runtime itself would.
+  CUcontext ctx = nullptr;
+  if (g_ctx_current(&ctx) != CUDA_SUCCESS) return nullptr;
+  int dev = 0;
+  if (ctx == nullptr && (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess))
+    return nullptr;
   return g_encode;
 }
 

@@ -4,7 +4,9 @@ import threading
 import pytest
 import torch
 
+import mixture_experts_ffn_05_b200 as mf
 from mixture_experts_ffn_05_b200 import train
+from tests.test_gpu_train_mlp import Case as MlpCase
 from tests.test_gpu_train_norm import Case as NormCase
 
 pytestmark = pytest.mark.gpu
@@ -61,5 +63,81 @@ def test_norms_of_few_and_many_rows(kind, which):
     torch.cuda.synchronize()
     assert refused == [0] * len(cases)
     for c, w in zip(cases, want):
+        for t, f in zip(outs(c), w):
+            assert torch.equal(t, f)
+
+
+def on_a_new_thread(body):
+    """body on a host thread that has not used the GPU before; what it raised."""
+    raised = []
+
+    def work():
+        try:
+            body()
+        except Exception as e:  # noqa: BLE001 - reported by the test
+            raised.append(repr(e))
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    return raised
+
+
+@pytest.mark.parametrize("T", [5, 700])
+def test_first_call_of_a_thread(T):
+    """Each entry point as a thread's very first use of the GPU."""
+    H, D = 512, 384
+    c = MlpCase(T, H, D, keep="int8").forward().backward()
+    cfg = mf.Config(hidden=H, num_experts=16, top_k=4, expert_inter=128, dense_inter=D)
+    out, ws = torch.empty(T, H, dtype=torch.bfloat16, device="cuda"), mf.workspace(cfg, T)
+    x = c.x.contiguous()
+    mf.dense_mlp_forward(cfg, x, c.wgu, c.wd, out, ws)
+    results = (c.y, c.gu.codes, c.dx, c.dwgu, c.dwd, out)
+    want = [t.clone() for t in results]
+    for t in results:
+        t.zero_()
+    torch.cuda.synchronize()
+    s = torch.cuda.current_stream()
+    assert on_a_new_thread(c.forward) == []
+    assert on_a_new_thread(c.backward) == []
+    assert on_a_new_thread(
+        lambda: mf.dense_mlp_forward(cfg, x, c.wgu, c.wd, out, ws, stream=s)) == []
+    for t, f in zip(results, want):
+        assert torch.equal(t, f)
+    n = NormCase(T, H, "layer").run()
+    want = n.dx.clone()
+    n.dx.zero_()
+    torch.cuda.synchronize()
+    assert on_a_new_thread(n.run) == []
+    assert torch.equal(n.dx, want)
+
+
+def test_mlps_of_few_and_many_tokens():
+    """Forward and backward passes of two sizes on two threads, over and over."""
+    cases = [MlpCase(T, 512, 384, keep="int8", seed=T).forward().backward() for T in (40, 1000)]
+    outs = lambda c: (c.y, c.dx, c.dwgu, c.dwd)  # noqa: E731
+    want = [[t.clone() for t in outs(c)] for c in cases]
+    torch.cuda.synchronize()
+    start, raised = threading.Barrier(len(cases)), []
+
+    def work(c):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                start.wait()
+                for _ in range(500):
+                    c.forward().backward()
+        except Exception as e:  # noqa: BLE001 - reported below
+            raised.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert raised == []
+    for c, w in zip(cases, want):
+        assert mf.moe_check_device_status(c.ws) == mf.MOE_OK
         for t, f in zip(outs(c), w):
             assert torch.equal(t, f)
