@@ -45,7 +45,13 @@ typedef enum {
  *   scale byte = k + 127, an all-zero group having byte 1.
  * A group that holds an infinity or NaN gets scale byte 255 and codes 0, and reads back as
  * NaN throughout.  Since s is a power of two, code * s is exact in bf16 (and in fp16 within
- * its normal range): reading a checkpoint adds no second rounding. */
+ * its normal range): reading a checkpoint adds no second rounding.
+ *
+ * code * s may lie a rounding above what a format holds.  Read back in 16 bits, values past
+ * the format's largest finite one become that one, so a finite 16-bit activation never reads
+ * back as an infinity (fp16: 65504 is kept as 64 * 2^10 and reads back as 65504).  In fp32,
+ * as F32 and where the backward passes compute, kept values of at least 2^128 (1 - 2^-7) for
+ * int8 and 2^128 (1 - 2^-5) for E4M3 are 2^128: infinity. */
 typedef struct {
   void* data;      /* elements of `format`, row r at element r * ld */
   uint8_t* scales; /* 8-bit formats: [rows][ceil(cols / 32)] scale bytes; else NULL */
@@ -54,7 +60,8 @@ typedef struct {
 } moe_act_t;
 
 /* Writes the 8-bit checkpoint `dst` of `src` (BF16, F16 or F32), and reads the checkpoint
- * `src` back into `dst` (BF16, F16 or F32, rounded to nearest even).
+ * `src` back into `dst` (BF16, F16 or F32, rounded to nearest even; see above for values past
+ * the largest).
  * rows >= 0, 1 <= cols <= 65536, rows * cols < 2^46. */
 moe_status_t moe_act_encode(int64_t rows, int32_t cols, const moe_act_t* src,
                             const moe_act_t* dst, void* stream);

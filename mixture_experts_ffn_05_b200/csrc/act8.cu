@@ -149,6 +149,35 @@ __global__ void __launch_bounds__(32 * kActWarps, kActCtas) act_encode_kernel(Ac
   }
 }
 
+// Values read back, rounded to nearest even.  A code times its scale may be a rounding above
+// the format's largest finite value (fp16: 65504 is kept as 64 2^10): 16-bit formats take that
+// largest value for anything past it, so that what was finite stays finite.  NaN stays NaN.
+template <int FMT>
+__device__ __forceinline__ uint32_t pack2_finite(float a, float b) {
+  uint32_t r;
+  if constexpr (FMT == kFmtF16)
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  else
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+template <int FMT>
+__device__ __forceinline__ void store8_finite(void* base, int64_t i, const float (&f)[8]) {
+  if constexpr (FMT == kFmtF32)
+    store8<FMT>(base, i, f);
+  else
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + i) =
+        make_uint4(pack2_finite<FMT>(f[0], f[1]), pack2_finite<FMT>(f[2], f[3]),
+                   pack2_finite<FMT>(f[4], f[5]), pack2_finite<FMT>(f[6], f[7]));
+}
+template <int FMT>
+__device__ __forceinline__ void store1_finite(void* base, int64_t i, float f) {
+  if constexpr (FMT == kFmtF32)
+    store1<FMT>(base, i, f);
+  else
+    static_cast<uint16_t*>(base)[i] = static_cast<uint16_t>(pack2_finite<FMT>(f, 0.f));
+}
+
 template <int FMT, bool WIDE, bool INT8>
 __global__ void __launch_bounds__(32 * kActWarps, kActCtas) act_decode_kernel(Act8Args a) {
   const int lane = threadIdx.x & 31;
@@ -178,7 +207,7 @@ __global__ void __launch_bounds__(32 * kActWarps, kActCtas) act_decode_kernel(Ac
         for (int i = 0; i < 2; ++i) {
           float f[8];
           decode8<INT8>(w[b][i], scale, f);
-          if (room[b] > 16 * i) store8<FMT>(vals[b], 16 * i, f);
+          if (room[b] > 16 * i) store8_finite<FMT>(vals[b], 16 * i, f);
         }
       }
     }
@@ -198,7 +227,7 @@ __global__ void __launch_bounds__(32 * kActWarps, kActCtas) act_decode_kernel(Ac
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int64_t c = c0 + 32 * i + lane;
-        if (c < a.cols) store1<FMT>(a.vals, r * a.ld_vals + c, f[i]);
+        if (c < a.cols) store1_finite<FMT>(a.vals, r * a.ld_vals + c, f[i]);
       }
     }
   }
