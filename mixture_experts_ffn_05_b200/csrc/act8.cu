@@ -238,8 +238,7 @@ static cudaError_t launch_act(const Act8Args& a, bool encode, bool wide, int gri
                               cudaStream_t s) {
   auto k = encode ? (wide ? act_encode_kernel<FMT, true, INT8> : act_encode_kernel<FMT, false, INT8>)
                   : (wide ? act_decode_kernel<FMT, true, INT8> : act_decode_kernel<FMT, false, INT8>);
-  k<<<grid, 32 * kActWarps, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_k(k, dim3(static_cast<unsigned>(grid)), dim3(32 * kActWarps), 0, s, false, a);
 }
 
 cudaError_t launch_act8(Act8Args a, int fmt, bool encode, cudaStream_t s) {

@@ -20,8 +20,7 @@ __global__ void __launch_bounds__(32) wait_selftest_kernel(unsigned* status, uin
 }
 
 cudaError_t launch_wait_selftest(unsigned* status, uint64_t timeout_ns, cudaStream_t s) {
-  wait_selftest_kernel<<<1, 32, 0, s>>>(status, timeout_ns);
-  return cudaGetLastError();
+  return launch_k(wait_selftest_kernel, dim3(1), dim3(32), 0, s, false, status, timeout_ns);
 }
 
 }  // namespace moe

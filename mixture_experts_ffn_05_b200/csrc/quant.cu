@@ -188,31 +188,31 @@ cudaError_t launch_quantize_nvfp4(const uint16_t* w, int64_t matrices, int64_t r
   const int64_t per_matrix = rows * cols;
   cudaError_t e = cudaMemsetAsync(tensor_scale, 0, static_cast<size_t>(matrices) * sizeof(float), s);
   if (e != cudaSuccess) return e;
+  auto of = [](int64_t items) { return dim3(static_cast<unsigned>((items + 255) / 256)); };
   const int64_t chunks = matrices * per_matrix / 8;
-  nvfp4_amax_kernel<<<static_cast<unsigned>((chunks + 255) / 256), 256, 0, s>>>(
-      per_matrix / 8, chunks, w, reinterpret_cast<unsigned*>(tensor_scale));
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_k(nvfp4_amax_kernel, of(chunks), dim3(256), 0, s, false, per_matrix / 8, chunks, w,
+               reinterpret_cast<unsigned*>(tensor_scale));
+  if (e != cudaSuccess) return e;
   const int64_t blocks = matrices * per_matrix / 16;
-  nvfp4_quant_kernel<<<static_cast<unsigned>((blocks + 255) / 256), 256, 0, s>>>(
-      per_matrix / 16, blocks, w, tensor_scale, q, bscale);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  nvfp4_tscale_kernel<<<static_cast<unsigned>((matrices + 255) / 256), 256, 0, s>>>(matrices,
-                                                                                 tensor_scale);
-  return cudaGetLastError();
+  e = launch_k(nvfp4_quant_kernel, of(blocks), dim3(256), 0, s, false, per_matrix / 16, blocks, w,
+               tensor_scale, q, bscale);
+  if (e != cudaSuccess) return e;
+  return launch_k(nvfp4_tscale_kernel, of(matrices), dim3(256), 0, s, false, matrices,
+                  tensor_scale);
 }
 
 cudaError_t launch_quantize_fp8(const uint16_t* w, int64_t rows, int cols, uint8_t* q,
                                 float* scales, cudaStream_t s) {
   const int64_t blocks = (rows + 7) / 8;
-  quantize_fp8_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(rows, cols, w, q, scales);
-  return cudaGetLastError();
+  return launch_k(quantize_fp8_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, false,
+                  rows, cols, w, q, scales);
 }
 
 cudaError_t launch_quantize_int8(const uint16_t* w, int64_t rows, int cols, int8_t* q,
                                  float* scales, cudaStream_t s) {
   const int64_t blocks = (rows + 7) / 8;
-  quantize_int8_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(rows, cols, w, q, scales);
-  return cudaGetLastError();
+  return launch_k(quantize_int8_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s,
+                  false, rows, cols, w, q, scales);
 }
 
 }  // namespace moe
