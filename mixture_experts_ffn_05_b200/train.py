@@ -128,6 +128,12 @@ def _first(t, name):
     return t.get_device(), shape[0], shape[1]
 
 
+def _i32(n):
+    """A size as an int32 argument.  ctypes would take it modulo 2^32; one that does not fit
+    becomes the largest, which the library refuses as unsupported."""
+    return n if -0x80000000 <= n <= 0x7FFFFFFF else 0x7FFFFFFF
+
+
 def _wrong_device(t, name, index):
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
@@ -222,14 +228,14 @@ def _checkpoint(kept):
 def moe_act_encode(x, kept: Act8, stream=None) -> None:
     """Write the 8-bit checkpoint of x [rows][cols] (bf16, fp16 or fp32)."""
     i, rows, cols = _first(_plain(x, "x"), "x")
-    _run("moe_act_encode", i, stream, rows, cols, _act(x, "x", i, rows, cols, None),
+    _run("moe_act_encode", i, stream, rows, _i32(cols), _act(x, "x", i, rows, cols, None),
          _act(_checkpoint(kept), "kept", i, rows, cols, None))
 
 
 def moe_act_decode(kept: Act8, out, stream=None) -> None:
     """Read an 8-bit checkpoint back into out [rows][cols] (bf16, fp16 or fp32)."""
     i, rows, cols = _first(_plain(out, "out"), "out")
-    _run("moe_act_decode", i, stream, rows, cols,
+    _run("moe_act_decode", i, stream, rows, _i32(cols),
          _act(_checkpoint(kept), "kept", i, rows, cols, None),
          _act(out, "out", i, rows, cols, None))
 
@@ -246,7 +252,7 @@ class NormConfig:
 
     def __post_init__(self):
         object.__setattr__(self, "_c", CNormConfig(
-            _KINDS[self.kind], self.cols, self.eps, _FORMATS[self.dtype],
+            _KINDS[self.kind], _i32(self.cols), self.eps, _FORMATS[self.dtype],
             _FORMATS[self.param_dtype]))
 
     def c(self) -> CNormConfig:
@@ -255,7 +261,7 @@ class NormConfig:
 
 def norm_workspace(cfg: NormConfig, T: int, device=None) -> torch.Tensor:
     """A zeroed workspace for moe_norm_backward over T rows."""
-    n = int(_lib().moe_norm_workspace_size(cfg._c, int(T)))
+    n = int(_lib().moe_norm_workspace_size(cfg._c, _i32(int(T))))
     return _zeros(n, "moe_norm_workspace_size", device)
 
 
@@ -265,7 +271,7 @@ def moe_norm_forward(cfg, x, gain, bias, y, mean, rstd, kept: Act8 | None = None
     norm only), and on request the 8-bit checkpoint of x.  gain and bias may be None."""
     i, T, _ = _first(_plain(x, "x"), "x")
     n, dt, pt, f32 = cfg.cols, cfg.dtype, cfg.param_dtype, torch.float32
-    _run("moe_norm_forward", i, stream, cfg._c, T, _act(x, "x", i, T, n, dt),
+    _run("moe_norm_forward", i, stream, cfg._c, _i32(T), _act(x, "x", i, T, n, dt),
          None if gain is None else _ptr(gain, "gain", i, pt, n),
          None if bias is None else _ptr(bias, "bias", i, pt, n),
          _act(_plain(y, "y"), "y", i, T, n, dt),
@@ -279,7 +285,7 @@ def moe_norm_backward(cfg, x, gain, mean, rstd, dy, dx, d_gain, d_bias, ws,
     checkpoint and the forward pass's statistics.  accumulate adds to d_gain and d_bias."""
     i, T, _ = _first(x, "x")
     n, dt, f32 = cfg.cols, cfg.dtype, torch.float32
-    _run("moe_norm_backward", i, stream, cfg._c, T, _act(x, "x", i, T, n, dt),
+    _run("moe_norm_backward", i, stream, cfg._c, _i32(T), _act(x, "x", i, T, n, dt),
          None if gain is None else _ptr(gain, "gain", i, cfg.param_dtype, n),
          None if mean is None else _ptr(mean, "mean", i, f32, T), _ptr(rstd, "rstd", i, f32, T),
          _act(_plain(dy, "dy"), "dy", i, T, n, dt), _act(_plain(dx, "dx"), "dx", i, T, n, dt),
@@ -298,8 +304,8 @@ class MlpConfig:
     dtype: torch.dtype = torch.bfloat16  # or torch.float16
 
     def __post_init__(self):
-        object.__setattr__(self, "_c", CMlpConfig(self.hidden, self.inter, _ACTS[self.act],
-                                                  _FORMATS[self.dtype]))
+        object.__setattr__(self, "_c", CMlpConfig(
+            _i32(self.hidden), _i32(self.inter), _ACTS[self.act], _FORMATS[self.dtype]))
 
     def c(self) -> CMlpConfig:
         return self._c
@@ -307,7 +313,7 @@ class MlpConfig:
 
 def mlp_workspace(cfg: MlpConfig, T: int, device=None) -> torch.Tensor:
     """A zeroed workspace for moe_mlp_forward and moe_mlp_backward over T rows."""
-    n = int(_lib().moe_mlp_workspace_size(cfg._c, int(T)))
+    n = int(_lib().moe_mlp_workspace_size(cfg._c, _i32(int(T))))
     return _zeros(n, "moe_mlp_workspace_size", device)
 
 
@@ -316,7 +322,7 @@ def moe_mlp_forward(cfg, x, w_gate_up, w_down, y, ws, kept_gu=None, stream=None)
     it, a [T][2D] tensor or an Act8 of two parts."""
     i, T, _ = _first(_plain(x, "x"), "x")
     H, D, dt = cfg.hidden, cfg.inter, cfg.dtype
-    _run("moe_mlp_forward", i, stream, cfg._c, T, _act(x, "x", i, T, H, dt),
+    _run("moe_mlp_forward", i, stream, cfg._c, _i32(T), _act(x, "x", i, T, H, dt),
          _ptr(w_gate_up, "w_gate_up", i, dt, 2 * D * H), _ptr(w_down, "w_down", i, dt, D * H),
          _act(_plain(y, "y"), "y", i, T, H, dt),
          None if kept_gu is None else _act(kept_gu, "kept_gu", i, T, D, dt, 2),
@@ -333,7 +339,7 @@ def moe_mlp_backward(cfg, x, gu, w_gate_up, w_down, dy, dx, dw_gate_up, dw_down,
     grad = next((g.dtype for g in (dw_gate_up, dw_down) if g is not None), dt)
     if grad not in (dt, torch.float32):
         raise TypeError(f"weight gradients must be {dt} or torch.float32, got {grad}")
-    _run("moe_mlp_backward", i, stream, cfg._c, T,
+    _run("moe_mlp_backward", i, stream, cfg._c, _i32(T),
          None if x is None and dw_gate_up is None else _act(x, "x", i, T, H, dt),
          _act(gu, "gu", i, T, D, dt, 2),
          None if w_gate_up is None and dx is None else
