@@ -12,7 +12,7 @@
  *     their columns.  The gaps between rows are neither read for results nor written.
  *   - Every tensor pointer is 16-byte aligned, scales excepted (any alignment).
  *   - Outputs must not overlap inputs or one another, unless a function says otherwise.
- *   - 0 <= T < 2^31 - 512 rows.  T = 0 computes nothing, but weight gradients that are not
+ *   - 0 <= T <= 2^31 - 512 rows.  T = 0 computes nothing, but weight gradients that are not
  *     accumulated are set to zero.
  *   - A workspace is 256-byte aligned and zeroed once before its first use; its first word
  *     is the status word that moe_check_device_status() reads.  Calls whose kernels may

@@ -76,3 +76,24 @@ def test_workspaces_and_configurations_past_32_bits(past):
                  (train.mlp_workspace, train.MlpConfig(64, past))):
         with pytest.raises(mf.MoeError):
             f(c, 4, device="cpu")
+
+
+def test_the_most_rows():
+    """2^31 - 512 rows, as the header says, and not one more (the tiles' rows stay int32)."""
+    mbuild.build()
+    most = (1 << 31) - 512
+    l = train._lib()
+    for f, c in ((l.moe_norm_workspace_size, train.NormConfig(8).c()),
+                 (l.moe_mlp_workspace_size, train.MlpConfig(8, 8).c())):
+        assert f(c, most) > 0 and f(c, most + 1) == 0
+    act = train.CAct(1 << 20, None, 8, train.F_BF16)
+    n, m = train.NormConfig(8).c(), train.MlpConfig(8, 8).c()
+    ptr = 1 << 20
+    # up to the limit it is the tensors (here: none) that are refused, past it the size
+    for T, want in ((most, mf.MOE_ERR_INVALID_ARG), (most + 1, mf.MOE_ERR_UNSUPPORTED)):
+        assert l.moe_norm_forward(n, T, None, None, None, act, None, ptr, None, None) == want
+        assert l.moe_norm_backward(n, T, None, None, None, ptr, act, act, None, None, 0, ptr,
+                                   1 << 40, None) == want
+        assert l.moe_mlp_forward(m, T, None, ptr, ptr, act, None, ptr, 1 << 50, None) == want
+        assert l.moe_mlp_backward(m, T, act, None, ptr, ptr, act, act, ptr, ptr, 0, 0, ptr,
+                                  1 << 50, None) == want
