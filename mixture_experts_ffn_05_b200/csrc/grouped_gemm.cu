@@ -108,7 +108,9 @@ struct Cfg {
   // tmem slot, abort, bcast x2, group piece broadcast 2 x 2, queue slots
   static constexpr int kMiscInts = 8 + kQ;
   static constexpr int kPreOff = kMiscOff + kMiscInts * 4;
-  static constexpr int kTabInts = 4 * kMaxEntries;  // pre, cnt, b0, ng
+  // token_rows comes with the narrowest tiles (at most 8 tokens)
+  static constexpr int kTok = BN == 16 && !W8 && !PAIR ? kTokenRows : 0;
+  static constexpr int kTabInts = 4 * kMaxEntries + kTok;  // pre, cnt, b0, ng, tok
   // output staging (transposes a warp's slice of the tile so that each lane stores 16 or
   // 32 contiguous bytes): two 1 KB buffers per epilogue warp (one where two do not fit
   // next to the pipeline)
@@ -250,6 +252,7 @@ __global__ void __launch_bounds__((Cfg<BN, W8, PAIR>::kThreads), 1)
   int* cnt = pre + kMaxEntries;
   int* b0 = cnt + kMaxEntries;
   int* ng = b0 + kMaxEntries;
+  int* tok = ng + kMaxEntries;           // [kTok] token of each sorted row (token_rows)
   uint8_t* stg_all = smem + C::kStgOff;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -304,8 +307,14 @@ __global__ void __launch_bounds__((Cfg<BN, W8, PAIR>::kThreads), 1)
   // Everything up to the producer's first token-tile load overlaps the previous kernel
   // on the stream.  The routing tables read here (offsets) come from kernels that
   // completed before that kernel started; only the token tiles (gathered rows, h) are
-  // its own results, and the producer loads them after the dependency wait.
+  // its own results, and the producer loads them after the dependency wait.  Where that
+  // kernel wrote the tables as well (token_rows), everything from here on waits for it; the
+  // next launch reads them early, so it may start only then.
+  const bool by_token = C::kTok > 0 && P.token_rows != nullptr;
+  if (by_token) pdl_wait();
   pdl_trigger();
+  if (by_token && static_cast<int>(threadIdx.x) < min(C::kTok, P.prob[0].n_tokens))
+    tok[threadIdx.x] = P.token_rows[threadIdx.x] / P.top_k;
   for (int i = threadIdx.x; i < nent; i += C::kThreads) {
     const int p = i < P.prob[0].groups ? 0 : 1;
     const int g = p == 0 ? i : i - P.prob[0].groups;
@@ -387,7 +396,7 @@ __global__ void __launch_bounds__((Cfg<BN, W8, PAIR>::kThreads), 1)
       // Weight tiles are never written by an earlier kernel, so the first ring fill of
       // them is issued before the dependency wait; the token-tile loads of those stages
       // are held here and issued after it.
-      bool waited = false;
+      bool waited = by_token;
       int nd = 0, steps = 0;
       uint8_t* d_dst[2 * C::kStages];
       const CUtensorMap* d_map[2 * C::kStages];
@@ -454,13 +463,23 @@ __global__ void __launch_bounds__((Cfg<BN, W8, PAIR>::kThreads), 1)
               tma_load_2d_pair(sa, ma, fb, ks * kw, arow, pol_w);
             load_b(sa + C::kABytes, mb, ks * kw, brow, &full[stage]);
           } else {
-            mbar_arrive_expect_tx(&full[stage], C::kABytes + nb * C::kBBytes);
+            const bool rows = by_token && pc.p == 0;
+            mbar_arrive_expect_tx(&full[stage],
+                                  C::kABytes + (rows ? pc.n_valid * 128 : nb * C::kBBytes));
             if (pr.kind == 0)  // 8 gate rows, the 8 matching up rows, ... (one 5-D box)
               tma_load_5d(sa, ma, &full[stage], ks * kw, 0, 0, pc.m * 8, pc.g, pol_w);
             else
               tma_load_2d(sa, ma, &full[stage], ks * kw, arow, pol_w);
-            for (int b = 0; b < nb; ++b)
-              load_b(sa + C::kABytes + b * C::kBBytes, mb, ks * kw + 64 * b, brow, &full[stage]);
+            if (rows) {
+              // one box of a row each; the tile's other rows keep what they held, and the
+              // accumulator's columns that come from those are never read
+              for (int r = 0; r < pc.n_valid; ++r)
+                tma_load_2d(sa + C::kABytes + r * 128, mb, &full[stage], ks * kw, tok[brow + r],
+                            pol_b);
+            } else {
+              for (int b = 0; b < nb; ++b)
+                load_b(sa + C::kABytes + b * C::kBBytes, mb, ks * kw + 64 * b, brow, &full[stage]);
+            }
           }
           armed[stage] = static_cast<int>(phase);
           if (++stage == C::kStages) {

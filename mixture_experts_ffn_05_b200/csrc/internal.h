@@ -54,6 +54,11 @@ struct GemmParams {
   int nprob;
   int int8_weights;     // a problem has int8 A: use the variant with converter warps
   int pairs;            // run on CTA pairs (see gemm_pairs_allowed)
+  // Few pairs (at most kTokenRows): problem 0's B operand is the tokens themselves, and row i of
+  // the sorted order is its row token_rows[i] / top_k.  The kernel directly before this one
+  // wrote these rows and the offsets.  NULL: the B operand's rows lie in sorted order.
+  const int* token_rows;
+  int top_k;
   float* partials;      // split-K partial tiles, [piece][BN][128] fp32
   unsigned* counters;   // split-K arrival counters, zero between launches
   unsigned* sched;      // [2] piece counter and finished CTAs (single-CTA launches), zero
@@ -61,6 +66,8 @@ struct GemmParams {
   unsigned* status;     // device status word
   uint64_t timeout_ns;  // bound of every wait
 };
+
+constexpr int kTokenRows = 32;
 
 struct GemmMaps {
   CUtensorMap a[2];  // weights of problem map 0 / 1
@@ -90,9 +97,7 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
 
 // Launchers.  All return cudaSuccess or the launch error.
 // Router + pre norms + top-k in one launch; when offsets != NULL (and T*k fits the
-// single-block sort, see permute_blocks) also the token-to-expert counting sort, and with
-// aperm != NULL (a single token block, T <= 8) the gather of the routed rows of xn_moe in
-// sorted order into aperm (fp16 when aperm_f16).
+// single-block sort, see permute_blocks) also the token-to-expert counting sort.
 // counters: router_counters(T) words, zero on entry (left zero on exit).
 cudaError_t launch_router(int T, int H, int E, int k, float eps, const uint16_t* x,
                           const uint16_t* router_scale, const uint16_t* w_router,
@@ -100,8 +105,7 @@ cudaError_t launch_router(int T, int H, int E, int k, float eps, const uint16_t*
                           const uint16_t* g_pre_moe, const uint16_t* g_pre_dense,
                           uint16_t* xn_moe, uint16_t* xn_dense, float* logits, int* topk_idx,
                           float* topk_w, unsigned* counters, unsigned* status, int* offsets,
-                          int* sorted_src, int* inv_pos, uint16_t* aperm, bool aperm_f16,
-                          cudaStream_t s, bool pdl = false);
+                          int* sorted_src, int* inv_pos, cudaStream_t s, bool pdl = false);
 int router_counters(int T);
 
 // The tensor-core router (router_tc.cu) serves batches of more than kRouterTcMinT

@@ -104,17 +104,16 @@ constexpr int kStreamMaxT = 256;
 
 bool stream_path(const Dims& d) { return d.nvfp4 || (d.int8 && d.T <= kStreamMaxT); }
 
-// Batches of at most this many (token, slot) pairs in one token block of the small-batch
-// router have their routed rows gathered by the router's last CTA, after its sort, instead
-// of by a launch of its own (a few rows: less than the launch and its kernel boundary;
-// bf16 T = 1 step 52.7 -> 50.8 us).  With int8 or NVFP4 experts it measured slower (T = 1
-// +4% and +7%: the weight-streaming GEMM's weight requests, issued before its dependency
-// wait, then overlap only the router's tail), and fp8 rows are quantised on the way, so
-// those keep the separate gather.
-constexpr int kRouterGatherMaxPairs = 32;
+// Batches of at most kTokenRows (token, slot) pairs in one token block of the small-batch
+// router have no gather: the gate_up launch loads each routed row of xn_moe where it lies.
+// It waits for the router before it can pick its pieces, where behind a gather it would fill
+// its ring meanwhile, and still takes less time: bf16 T = 1, 2, 4 in 51.2, 65.6, 89.6 us
+// against 52.6, 66.9, 90.4 with the gather as a launch of its own.  The weight-streaming
+// kernel (int8, NVFP4) and the quantised rows of fp8 need the gather.
+constexpr int kDirectMaxTokens = 8;
 
-bool router_gathers(const Dims& d) {
-  return d.T <= 8 && d.T * d.k <= kRouterGatherMaxPairs && !d.fp8 && !d.int8 && !d.nvfp4;
+bool rows_direct(const Dims& d) {
+  return d.T <= kDirectMaxTokens && d.T * d.k <= kTokenRows && !d.fp8 && !d.int8 && !d.nvfp4;
 }
 
 // K pieces of the weight-streaming kernel's tiles.  Pieces are dealt round-robin, so the
@@ -388,6 +387,7 @@ struct GemmJob {
   bool experts;
   const void* a_rows;        // gathered xn_moe rows, [Tk][H]: bf16, fp16 (int8 experts)
                              // or E4M3 codes (fp8 experts)
+  bool direct;               // a_rows is xn_moe itself, [T][H] (rows_direct)
   const float* a_scales;     // fp8: the gathered rows' scales [Tk]
   const void* w_gate_up;
   const void* w_down;
@@ -478,8 +478,8 @@ moe_status_t run_stream_gemms(const Dims& d, const Layout& L, void* ws, const Ge
 
 // The counters in the workspace start at zero (the caller zeroes a new workspace once)
 // and every kernel that uses one returns it to zero, so no call clears them.
-// first_kernel: the gate_up launch is no dependent launch on whatever the stream ran before
-// (the entry point's first kernel, or one that reads the previous kernel's tables early).
+// first_kernel: the gate_up launch is the entry point's first kernel (no dependent
+// launch on whatever the stream ran before).
 moe_status_t run_gemms(const Dims& d, const Layout& L, void* ws, const GemmJob& j,
                        cudaStream_t s, bool first_kernel, void* const* ev = nullptr) {
   if (stream_path(d)) return run_stream_gemms(d, L, ws, j, s, first_kernel, ev);
@@ -495,6 +495,8 @@ moe_status_t run_gemms(const Dims& d, const Layout& L, void* ws, const GemmJob& 
   // into fp16 in tensor memory; the bf16 dense MLP in the same launch reads its A tiles
   // from shared memory as usual).
   const bool w8 = j.experts && d.int8;
+  gu.token_rows = j.direct ? j.sorted_src : nullptr;
+  gu.top_k = d.k;
   gu.sched = at<unsigned>(ws, L.sched);
   dn.sched = at<unsigned>(ws, L.sched) + 2;  // the down launch may start before gate_up ends
   for (GemmParams* P : {&gu, &dn}) {
@@ -550,7 +552,8 @@ moe_status_t run_gemms(const Dims& d, const Layout& L, void* ws, const GemmJob& 
     const bool w1 = d.int8 || d.fp8;
     if (!encode_gate_up(&mgu.a[np], j.w_gate_up, d.E, d.I, d.H, w1) ||
         !(d.fp8 ? encode_i8(&mgu.b[np], j.a_rows, Tk, d.H, bbox_gu)
-                : encode_bf16(&mgu.b[np], j.a_rows, Tk, d.H, bbox_gu)) ||
+                : j.direct ? encode_bf16(&mgu.b[np], j.a_rows, d.T, d.H, 1)
+                           : encode_bf16(&mgu.b[np], j.a_rows, Tk, d.H, bbox_gu)) ||
         !encode_a(&mdn.a[np], j.w_down, static_cast<int64_t>(d.E) * d.H, d.I, 128, w1) ||
         !(d.fp8 ? encode_i8(&mdn.b[np], at<uint8_t>(ws, L.h8), Tk, d.I, bbox_dn)
                 : encode_bf16(&mdn.b[np], h, Tk, d.I, bbox_dn)))
@@ -614,8 +617,6 @@ struct RouteJob {
   int* offsets;  // with sorted_src and inv_pos: sort the pairs in the same launch; or NULL
   int* sorted_src;
   int* inv_pos;
-  uint16_t* aperm;  // with the sort: gather the routed rows there too (router_gathers); or NULL
-  bool aperm_f16;
 };
 
 // The router step, launched as the first kernel of the entry point: the tensor-core
@@ -631,12 +632,11 @@ moe_status_t run_router(const Dims& d, const Layout& L, void* ws, const RouteJob
                                      r.logit_bias, r.per_expert_scale, r.g_pre_moe,
                                      r.g_pre_dense, r.xn_moe, r.xn_dense,
                                      at<float>(ws, L.logits), r.topk_idx, r.topk_w, counters,
-                                     status, r.offsets, r.sorted_src, r.inv_pos, r.aperm,
-                                     r.aperm_f16, s));
+                                     status, r.offsets, r.sorted_src, r.inv_pos, s));
   uint16_t* whi = at<uint16_t>(ws, L.wr_hi);
   uint16_t* wlo = at<uint16_t>(ws, L.wr_lo);
   const int ne = (d.E + 15) / 16 * 16 / router_tc_slices(d.T, d.E);  // experts per CTA
-  if (r.offsets != nullptr || r.aperm != nullptr) return MOE_ERR_INVALID_ARG;  // not on this path
+  if (r.offsets != nullptr) return MOE_ERR_INVALID_ARG;  // not on this path
   RouterTcMaps m;
   if (!encode_bf16(&m.x, r.x, d.T, d.H, 128) || !encode_bf16(&m.whi, whi, d.E, d.H, ne) ||
       !encode_bf16(&m.wlo, wlo, d.E, d.H, ne))
@@ -681,7 +681,7 @@ int32_t moe_block_launch_count(const moe_config_t* cfg, int32_t T) {
   int n = tc ? 2 : 1;                                     // router (prep + router)
   if (!fused_sort) n += permute_blocks(Tk) == 0 ? 1 : 3;  // permutation
   if (d.fp8) n += 1;                                      // h quantised for the down matmul
-  if (!(fused_sort && router_gathers(d))) n += 1;         // gather
+  if (!(fused_sort && rows_direct(d))) n += 1;         // gather
   return n + 3;                                           // gate_up, down, combine
 }
 
@@ -840,11 +840,10 @@ moe_status_t moe_block_forward(const moe_config_t* cfg, int32_t T, const moe_bf1
       if (ev[i] == nullptr) return MOE_ERR_INVALID_ARG;
   if (!mark(ev, 0, s)) return MOE_ERR_CUDA;
   const bool fused_sort = !router_uses_tc(d.T) && permute_blocks(Tk) == 0;
-  const bool rgather = fused_sort && router_gathers(d);
+  const bool direct = fused_sort && rows_direct(d);
   const RouteJob r{x, w->router_scale, w->w_router, w->logit_bias, w->per_expert_scale,
                    w->g_pre_moe, w->g_pre_dense, topk_idx, topk_w, xn_moe, xn_dense,
-                   fused_sort ? offsets : nullptr, sorted, inv,
-                   rgather ? aperm : nullptr, false};
+                   fused_sort ? offsets : nullptr, sorted, inv};
   if ((st = run_router(d, L, ws, r, s)) != MOE_OK) return st;
   if (!mark(ev, 1, s)) return MOE_ERR_CUDA;
   if (!fused_sort &&
@@ -852,12 +851,13 @@ moe_status_t moe_block_forward(const moe_config_t* cfg, int32_t T, const moe_bf1
                                        at<int>(ws, L.bbase), s, true))) != MOE_OK)
     return st;
   if (!mark(ev, 2, s)) return MOE_ERR_CUDA;
-  if (!rgather && (st = gather_tokens(d, L, ws, sorted, inv, xn_moe, s, true)) != MOE_OK)
+  if (!direct && (st = gather_tokens(d, L, ws, sorted, inv, xn_moe, s, true)) != MOE_OK)
     return st;
   if (!mark(ev, 3, s)) return MOE_ERR_CUDA;
   GemmJob j{};
   j.experts = true;
-  j.a_rows = aperm;
+  j.a_rows = direct ? xn_moe : aperm;
+  j.direct = direct;
   j.a_scales = at<float>(ws, L.sx);
   j.w_gate_up = w->experts.w_gate_up;
   j.w_down = w->experts.w_down;
@@ -876,9 +876,9 @@ moe_status_t moe_block_forward(const moe_config_t* cfg, int32_t T, const moe_bf1
   j.dense_out = dense;
   j.dense_f32 = 1;
   // The GEMM launch reads the routing tables before its dependency wait, which is right only
-  // if they come from a kernel that completed before the one it follows could start.  When
-  // the router also gathers, it is that one: the gate_up launch must then wait for it whole.
-  if ((st = run_gemms(d, L, ws, j, s, rgather, ev)) != MOE_OK) return st;
+  // if they come from a kernel that completed before the one it follows could start.  Without
+  // a gather in between the router is that one: the tables are then read after the wait.
+  if ((st = run_gemms(d, L, ws, j, s, false, ev)) != MOE_OK) return st;
   if ((st = cuda_status(launch_combine_block(d.T, d.H, d.k, d.eps, x, y, inv, nullptr, topk_w,
                                              dense, w->g_post_moe,
                                              w->g_post_dense, w->g_post_ff, out, moe_out, s,
