@@ -98,7 +98,7 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
 // Launchers.  All return cudaSuccess or the launch error.
 // Router + pre norms + top-k in one launch; when offsets != NULL (and T*k fits the
 // single-block sort, see permute_blocks) also the token-to-expert counting sort.
-// counters: router_counters(T) words, zero on entry (left zero on exit).
+// counters: a word per token block of 8 and one more, zero on entry (left zero on exit).
 cudaError_t launch_router(int T, int H, int E, int k, float eps, const uint16_t* x,
                           const uint16_t* router_scale, const uint16_t* w_router,
                           const float* bias, const uint16_t* per_expert_scale,
@@ -106,7 +106,6 @@ cudaError_t launch_router(int T, int H, int E, int k, float eps, const uint16_t*
                           uint16_t* xn_moe, uint16_t* xn_dense, float* logits, int* topk_idx,
                           float* topk_w, unsigned* counters, unsigned* status, int* offsets,
                           int* sorted_src, int* inv_pos, cudaStream_t s, bool pdl = false);
-int router_counters(int T);
 
 // The tensor-core router (router_tc.cu) serves batches of more than kRouterTcMinT
 // tokens.  It needs two E x H bf16 buffers for the split W' = s * W_r / sqrt(H), the

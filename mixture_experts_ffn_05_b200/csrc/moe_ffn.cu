@@ -121,10 +121,20 @@ bool rows_direct(const Dims& d) {
 // of the launch (five CTAs per SM assumed), at least 32 KB and four K items each.
 constexpr int kStreamAssumedCtas = 5 * kAssumedSms;
 
+// Words of a workspace that must be zero between calls, at the same place for every batch
+// size and configuration, so that no call finds another one's data in them: the last-CTA
+// chains of the routers (one word a token block or tile: at most 17 of the small-batch
+// router's, 74 of the tensor-core router's, which has several slices up to there), the piece
+// counters of the two GEMM launches, and one word per split tile.  Launches split K when they
+// have few tiles (choose_split: 8 * 148 expected, which bounds the pieces by about 23500;
+// stream_splits: a few pieces a CTA); one with more tiles than words does not split.
+constexpr int kRouterWords = 256;
+constexpr int kCounterWords = 65536;
+
 struct StreamSplits {
   int gu_e, gu_d, dn_e, dn_d;  // K pieces: gate_up experts / dense, down experts / dense
   int nt_e, nt_d;              // token n-tiles of 8 per unit: experts / dense (both launches)
-  int64_t units, pieces;       // upper bounds over the two launches
+  int64_t pieces;              // upper bound over the two launches
   int64_t partial_floats;      // upper bound of the split-K partials of one launch
 };
 
@@ -172,7 +182,7 @@ StreamSplits stream_splits(const Dims& d) {
   const int64_t ch_e = std::min<int64_t>(d.E, Tk) + ceil_div(Tk, nc_e);
   const int64_t ch_d = ceil_div(T, nc_d);
   const int64_t u_gu = ch_e * tiles_gu_e + ch_d * tiles_gu_d, u_dn = (ch_e + ch_d) * tiles_dn;
-  ss.units = std::max(u_gu, u_dn);
+  if (std::max(u_gu, u_dn) > kCounterWords) ss.gu_e = ss.gu_d = ss.dn_e = ss.dn_d = 1;
   const int64_t p_gu_e = ch_e * tiles_gu_e * ss.gu_e, p_gu_d = ch_d * tiles_gu_d * ss.gu_d;
   const int64_t p_dn_e = ch_e * tiles_dn * ss.dn_e, p_dn_d = ch_d * tiles_dn * ss.dn_d;
   ss.pieces = std::max(p_gu_e + p_gu_d, p_dn_e + p_dn_d);
@@ -186,7 +196,6 @@ struct Layout {
   size_t status, rcounters, counters, logits, bhist, bbase, topk_idx, topk_w, offsets, sorted, inv;
   size_t xn_moe, xn_dense, aperm, h, y, hd, dense, partials, wr_hi, wr_lo, sched, total;
   size_t sx, h8, sh;  // fp8: token-row scales of the gathered rows, h in E4M3, h's scales
-  size_t counters_bytes;
   int bn, split_gu, split_dgu, split_d, split_dd;
   StreamSplits ss;    // the weight-streaming kernel's splits (stream_path only)
 };
@@ -208,18 +217,17 @@ Layout layout_of(const Dims& d) {
   // Upper bound of the N tiles: every non-empty expert has a partial tile.
   const int64_t ntl_e = std::min<int64_t>(d.E, Tk) + ceil_div(Tk, L.bn);
   const int64_t ntl_d = ceil_div(T, L.bn);
-  const int64_t pieces_gu = (d.I / 64) * ntl_e * L.split_gu + (d.D / 64) * ntl_d * L.split_dgu;
-  const int64_t pieces_dn = (d.H / 128) * ntl_e * L.split_d + (d.H / 128) * ntl_d * L.split_dd;
-  int64_t pieces = std::max(pieces_gu, pieces_dn);
-  bool any_split = L.split_gu > 1 || L.split_dgu > 1 || L.split_d > 1 || L.split_dd > 1;
+  const int64_t pieces =
+      std::max((d.I / 64) * ntl_e * L.split_gu + (d.D / 64) * ntl_d * L.split_dgu,
+               (d.H / 128) * ntl_e * L.split_d + (d.H / 128) * ntl_d * L.split_dd);
+  if (pieces > kCounterWords) L.split_gu = L.split_dgu = L.split_d = L.split_dd = 1;
+  const bool any_split = L.split_gu > 1 || L.split_dgu > 1 || L.split_d > 1 || L.split_dd > 1;
   int64_t partial_bytes = any_split ? pieces * L.bn * 128 * 4 : 0;
   if (stream_path(d)) {
     // the weight-streaming kernel: one counter per (tile, chunk), [64][8] fp32 per piece
     L.ss = stream_splits(d);
-    pieces = std::max(pieces, L.ss.units);
     const bool ssplit = L.ss.gu_e > 1 || L.ss.gu_d > 1 || L.ss.dn_e > 1 || L.ss.dn_d > 1;
     if (ssplit) partial_bytes = std::max<int64_t>(partial_bytes, L.ss.partial_floats * 4);
-    any_split = any_split || ssplit;
   }
   const int nb = permute_blocks(static_cast<int>(Tk));
 
@@ -229,12 +237,11 @@ Layout layout_of(const Dims& d) {
     off = align_up(off + std::max<size_t>(bytes, 1), kAlign);
     return at;
   };
-  // status word, router counters and GEMM counters are contiguous: one memset clears them
   L.status = 0;
   L.rcounters = 256;
-  L.counters = align_up(L.rcounters + static_cast<size_t>(router_counters(d.T)) * 4, 256);
-  L.counters_bytes = static_cast<size_t>(pieces) * 4;
-  off = align_up(L.counters + L.counters_bytes, kAlign);
+  L.sched = L.rcounters + kRouterWords * 4;  // [0..1] gate_up, [2..3] down
+  L.counters = L.sched + 256;
+  off = align_up(L.counters + kCounterWords * 4, kAlign);
   L.logits = take(static_cast<size_t>(T) * d.E * 4);
   L.bhist = take(static_cast<size_t>(nb) * d.E * 4);
   L.bbase = take(static_cast<size_t>(nb) * d.E * 4);
@@ -255,7 +262,6 @@ Layout layout_of(const Dims& d) {
   const size_t wr_bytes = router_uses_tc(d.T) ? static_cast<size_t>(d.E) * d.H * 2 : 0;
   L.wr_hi = take(wr_bytes);
   L.wr_lo = take(wr_bytes);
-  L.sched = take(16);  // the GEMM launches' piece counters: [0..1] gate_up, [2..3] down
   // fp8: the gathered rows' E4M3 codes share the aperm buffer; their scales, h in E4M3
   // and h's row scales
   L.sx = take(d.fp8 ? Tk * 4 : 0);

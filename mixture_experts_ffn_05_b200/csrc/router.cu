@@ -355,8 +355,6 @@ static cudaError_t launch_eb(const RouterArgs& a, cudaStream_t s, bool pdl) {
   return launch_k(router_kernel<EB>, grid, dim3(kRThreads), smem, s, pdl, a);
 }
 
-int router_counters(int T) { return (T + kRT - 1) / kRT + 1; }
-
 cudaError_t launch_router(int T, int H, int E, int k, float eps, const uint16_t* x,
                           const uint16_t* router_scale, const uint16_t* w_router,
                           const float* bias, const uint16_t* per_expert_scale,
