@@ -903,9 +903,12 @@ size_t moe_stack_workspace_size(const moe_config_t* cfg, int32_t chunk_tokens) {
   Dims d;
   const int32_t c = moe_stack_chunk_tokens(chunk_tokens);
   if (check_cfg(cfg, c, &d) != MOE_OK) return 0;
-  // the block's workspace, then two [chunk][H] bf16 buffers for the residual chain
-  const size_t block = align_up(layout_of(d).total, kAlign);
-  return block + 2 * align_up(static_cast<size_t>(c) * d.H * 2, kAlign);
+  // the block's workspace, then two [chunk][H] bf16 buffers for the residual chain.  The last
+  // chunk may have any length, and a shorter one may take more (it may split K).
+  const size_t rows = 2 * align_up(static_cast<size_t>(c) * d.H * 2, kAlign);
+  size_t block = 0;
+  for (d.T = c; d.T > 0; --d.T) block = std::max(block, layout_of(d).total);
+  return align_up(block, kAlign) + rows;
 }
 
 moe_status_t moe_stack_forward(const moe_config_t* cfg, int32_t T, const moe_bf16_t* x,
@@ -919,11 +922,17 @@ moe_status_t moe_stack_forward(const moe_config_t* cfg, int32_t T, const moe_bf1
   if (T < 0 || n_layers < 1 || layers == nullptr) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (x == nullptr || out == nullptr || !aligned16(x) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
-  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 ||
-      ws_bytes < moe_stack_workspace_size(cfg, chunk_tokens))
-    return MOE_ERR_WORKSPACE;
-  const size_t block = align_up(layout_of(d).total, kAlign);
+  // this call's chunk lengths alone (moe_stack_workspace_size covers every one)
+  d.T = std::min(c, T);
+  size_t block = layout_of(d).total;
+  if (T > c && T % c != 0) {
+    d.T = T % c;
+    block = std::max(block, layout_of(d).total);
+  }
+  block = align_up(block, kAlign);
   const size_t buf = align_up(static_cast<size_t>(c) * d.H * 2, kAlign);
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || ws_bytes < block + 2 * buf)
+    return MOE_ERR_WORKSPACE;
   moe_bf16_t* ping[2] = {at<moe_bf16_t>(ws, block), at<moe_bf16_t>(ws, block + buf)};
   for (int32_t t0 = 0; t0 < T; t0 += c) {
     const int32_t n = std::min(c, T - t0);
