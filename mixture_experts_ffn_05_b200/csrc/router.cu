@@ -332,7 +332,8 @@ __global__ void __launch_bounds__(kRThreads, 1) router_kernel(const RouterArgs a
   permute_block<kRThreads>(a.T * a.k, E, a.topk_idx, a.offsets, a.sorted_src, a.inv_pos, ps);
 }
 
-// Dynamic shared memory of a CTA with EB experts.
+// Dynamic shared memory of a CTA with EB experts, and the most of any (H <= 6144).
+constexpr int kRSmemBudget = 176 * 1024;
 static size_t router_smem(int H, int EB) { return static_cast<size_t>(kRT + EB + 1) * (H + 16) * 2; }
 
 // Experts per CTA: about one CTA per SM (token blocks x expert slices), within the
@@ -341,15 +342,17 @@ static int router_eb(int T, int H, int E) {
   const int tb = (T + kRT - 1) / kRT;
   int eb = 1;
   while (eb < kRMaxEB && tb * ((E + eb - 1) / eb) > 160) eb *= 2;
-  while (eb > 1 && router_smem(H, eb) > 176 * 1024) eb /= 2;
+  while (eb > 1 && router_smem(H, eb) > kRSmemBudget) eb /= 2;
   return eb;
 }
 
 template <int EB>
 static cudaError_t launch_eb(const RouterArgs& a, cudaStream_t s, bool pdl) {
   const size_t smem = router_smem(a.H, EB);
+  // the same limit for every call: one with a smaller H on another host thread may come
+  // between this and the launch
   cudaError_t e = cudaFuncSetAttribute(router_kernel<EB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+                                       kRSmemBudget);
   if (e != cudaSuccess) return e;
   dim3 grid((a.T + kRT - 1) / kRT, (a.E + EB - 1) / EB);
   return launch_k(router_kernel<EB>, grid, dim3(kRThreads), smem, s, pdl, a);

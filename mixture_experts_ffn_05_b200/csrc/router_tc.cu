@@ -571,9 +571,10 @@ int router_tc_slices(int T, int E) {
 template <int KMAX>
 static cudaError_t launch_tc(const RouterTcMaps& maps, const RouterTcArgs& a, size_t smem,
                              cudaStream_t s) {
+  // the same limit for every call (see launch_eb in router.cu)
   cudaError_t e = cudaFuncSetAttribute(router_tc_kernel<KMAX>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+                                       kTcSmemBudget + 1024);
   if (e != cudaSuccess) return e;
   return launch_k(router_tc_kernel<KMAX>,
                   dim3((a.T + kTcTokens - 1) / kTcTokens, a.slices), dim3(kTcThreads), smem, s,

@@ -1,4 +1,5 @@
 """Calls from several host threads at once, each with tensors, workspaces and a stream of its own."""
+import ctypes
 import threading
 
 import pytest
@@ -65,6 +66,50 @@ def test_norms_of_few_and_many_rows(kind, which):
     for c, w in zip(cases, want):
         for t, f in zip(outs(c), w):
             assert torch.equal(t, f)
+
+
+@pytest.mark.parametrize("T", [8, 200])
+def test_routers_of_narrow_and_wide_layers(T):
+    """The routers' kernels with the shared memory of two layer widths (T = 8) and of two expert
+    counts (T = 200, the tensor-core router)."""
+    sizes = [(512, 32), (2816, 128)] * 2
+    calls, outs = [], []
+    for i, (H, E) in enumerate(sizes):
+        cfg = mf.Config(hidden=H, num_experts=E, top_k=4, expert_inter=128, dense_inter=128)
+        g = torch.Generator(device="cuda").manual_seed(i)
+        t = {n: torch.randn(*sh, generator=g, device="cuda").bfloat16()
+             for n, sh in (("x", (T, H)), ("rs", (H,)), ("wr", (E, H)), ("pes", (E,)),
+                           ("gm", (H,)), ("gd", (H,)))}
+        idx = torch.zeros(T, 4, dtype=torch.int32, device="cuda")
+        w = torch.zeros(T, 4, device="cuda")
+        xm, xd = torch.zeros_like(t["x"]), torch.zeros_like(t["x"])
+        ws = mf.workspace(cfg, T)
+        mf.moe_router(cfg, t["x"], t["rs"], t["wr"], None, t["pes"], t["gm"], t["gd"], idx, w, xm,
+                      xd, ws)
+        outs.append([(o, o.clone()) for o in (idx, w, xm, xd)] + [(ws, None), (t, None)])
+        calls.append((cfg.c(), T, *(p.data_ptr() for p in (t["x"], t["rs"], t["wr"])), None,
+                      *(p.data_ptr() for p in (t["pes"], t["gm"], t["gd"], idx, w, xm, xd, ws)),
+                      ws.numel()))
+    torch.cuda.synchronize()
+    start, refused = threading.Barrier(len(calls)), []
+    fn = mf.lib().moe_router
+
+    def work(args, stream):
+        args = (ctypes.byref(args[0]), *args[1:], stream.cuda_stream)
+        start.wait()
+        refused.append(sum(fn(*args) != 0 for _ in range(3000)))
+
+    streams = [torch.cuda.Stream() for _ in calls]
+    threads = [threading.Thread(target=work, args=a) for a in zip(calls, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert refused == [0] * len(calls)
+    for o in outs:
+        for got, want in o[:4]:
+            assert torch.equal(got, want)
 
 
 def on_a_new_thread(body):
