@@ -45,6 +45,8 @@
 //     subnormals and normals line up with E2M1's); times the block scale the product is
 //     still exact in fp16 (at most 6 significant bits, a multiple of 2^-24, at most 0.17);
 //     2^14 and the matrix scale multiply the fp32 sum.  Tokens are fp16.
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "warp_mma.cuh"
@@ -745,16 +747,19 @@ cudaError_t launch_stream_gemm(const StreamParams& p, int sms, cudaStream_t s, b
 }
 
 int stream_gemm_ctas(int sms) {
-  static int per_sm = 0;  // CTAs resident per SM (the kernel's resources decide it)
+  // the limit belongs to the current device's copy of the kernel, so every call sets it
+  if (cudaFuncSetAttribute(stream_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kStreamRingBytes) != cudaSuccess)
+    return 0;
+  static std::atomic<int> resident{0};  // CTAs per SM (the kernel's resources decide it)
+  int per_sm = resident.load(std::memory_order_relaxed);
   if (per_sm == 0) {
-    if (cudaFuncSetAttribute(stream_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kStreamRingBytes) != cudaSuccess)
-      return 0;
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, stream_gemm_kernel, kStreamThreads,
                                                       kStreamRingBytes) != cudaSuccess)
       return 0;
     per_sm = n > 0 ? n : 1;
+    resident.store(per_sm, std::memory_order_relaxed);
   }
   return sms * per_sm;
 }
