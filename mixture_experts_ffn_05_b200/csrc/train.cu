@@ -217,6 +217,44 @@ Plan plan_products(const Product* pr, int n, int kind) {
   return best;
 }
 
+// The products of either pass; p points at what the call was given (NULL where only the sizes
+// matter).
+struct MlpTensors {
+  const void *x, *w_gate_up, *w_down, *dy;
+  int64_t ld_x, ld_dy;
+  void *h, *dgu;
+};
+Product up_product(const moe_mlp_config_t* c, int32_t T, const MlpLayout& L, const MlpTensors& p) {
+  const int64_t H = c->hidden, D = c->inter;
+  return Product{T, D, H, {p.x, p.ld_x, false}, {p.w_gate_up, H, false}, p.h, L.ld_h, 0, 0};
+}
+Product down_product(const moe_mlp_config_t* c, int32_t T, const MlpLayout& L, const MlpTensors& p,
+                     void* y, int64_t ld_y) {
+  const int64_t H = c->hidden, D = c->inter;
+  return Product{T, H, D, {p.h, L.ld_h, false}, {p.w_down, D, false}, y, ld_y, 0, 0};
+}
+Product dh_product(const moe_mlp_config_t* c, int32_t T, const MlpLayout& L, const MlpTensors& p,
+                   bool keep_h) {
+  const int64_t H = c->hidden, D = c->inter;
+  return Product{T, D, H, {p.dy, p.ld_dy, false}, {p.w_down, D, true}, keep_h ? p.h : nullptr,
+                 L.ld_h, 0, 0};
+}
+Product dx_product(const moe_mlp_config_t* c, int32_t T, const MlpLayout& L, const MlpTensors& p,
+                   void* dx, int64_t ld_dx) {
+  const int64_t H = c->hidden, D = c->inter;
+  return Product{T, H, 2 * D, {p.dgu, L.ld_dgu, false}, {p.w_gate_up, H, true}, dx, ld_dx, 0, 0};
+}
+Product dw_gate_up_product(const moe_mlp_config_t* c, int32_t T, const MlpLayout& L,
+                           const MlpTensors& p, void* dw, int f32, int acc) {
+  const int64_t H = c->hidden, D = c->inter;
+  return Product{2 * D, H, T, {p.dgu, L.ld_dgu, true}, {p.x, p.ld_x, true}, dw, H, f32, acc};
+}
+Product dw_down_product(const moe_mlp_config_t* c, int32_t T, const MlpLayout& L,
+                        const MlpTensors& p, void* dw, int f32, int acc) {
+  const int64_t H = c->hidden, D = c->inter;
+  return Product{H, D, T, {p.dy, p.ld_dy, true}, {p.h, L.ld_h, true}, dw, D, f32, acc};
+}
+
 moe_status_t run_products(const Product* pr, int n, TgParams p, cudaStream_t s, bool pdl) {
   const int sms = device_sm_count();
   if (sms <= 0) return MOE_ERR_CUDA;
@@ -261,6 +299,9 @@ moe_status_t run_products(const Product* pr, int n, TgParams p, cudaStream_t s, 
 bool gu_ok(const moe_act_t* gu, const moe_mlp_config_t* c) {
   return act_ok(gu, 2 * static_cast<int64_t>(c->inter), c->format, true) && gu->ld % 8 == 0;
 }
+
+// dx in a launch of its own, whose K loop is split, and not with the weight gradients.
+bool dx_alone(const Product& dx) { return plan_products(&dx, 1, kTgStore).small; }
 
 TgParams mlp_params(const moe_mlp_config_t* c, int kind, const moe_act_t* gu, void* ws) {
   TgParams p{};
@@ -378,7 +419,7 @@ moe_status_t moe_mlp_forward(const moe_mlp_config_t* cfg, int32_t T, const moe_a
   moe_status_t st = check_mlp(cfg, T);
   if (st != MOE_OK) return st;
   if (T == 0) return MOE_OK;
-  const int64_t H = cfg->hidden, D = cfg->inter;
+  const int64_t H = cfg->hidden;
   if (!act_ok(x, H, cfg->format, false) || !act_ok(y, H, cfg->format, false) || x->ld % 8 ||
       y->ld % 8 || !tensor_ok(w_gate_up) || !tensor_ok(w_down) ||
       (kept_gu != nullptr && !gu_ok(kept_gu, cfg)))
@@ -386,11 +427,11 @@ moe_status_t moe_mlp_forward(const moe_mlp_config_t* cfg, int32_t T, const moe_a
   const MlpLayout L = mlp_layout(cfg, T);
   if (!ws_ok(ws, ws_bytes, L.total)) return MOE_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  void* h = at<void>(ws, L.h);
-  const Product up{T, D, H, {x->data, x->ld, false}, {w_gate_up, H, false}, h, L.ld_h, 0, 0};
+  const MlpTensors p{x->data, w_gate_up, w_down, nullptr, x->ld, 0, at<void>(ws, L.h), nullptr};
+  const Product up = up_product(cfg, T, L, p);
   if ((st = run_products(&up, 1, mlp_params(cfg, kTgGluFwd, kept_gu, ws), s, false)) != MOE_OK)
     return st;
-  const Product down{T, H, D, {h, L.ld_h, false}, {w_down, D, false}, y->data, y->ld, 0, 0};
+  const Product down = down_product(cfg, T, L, p, y->data, y->ld);
   return run_products(&down, 1, mlp_params(cfg, kTgStore, nullptr, ws), s, true);
 }
 
@@ -424,38 +465,59 @@ moe_status_t moe_mlp_backward(const moe_mlp_config_t* cfg, int32_t T, const moe_
   const MlpLayout L = mlp_layout(cfg, T);
   if (!ws_ok(ws, ws_bytes, L.total)) return MOE_ERR_WORKSPACE;
   if (dx == nullptr && dw_gate_up == nullptr && dw_down == nullptr) return MOE_OK;
-  void *h = at<void>(ws, L.h), *dgu = at<void>(ws, L.dgu);
-  const void* x16 = x != nullptr ? x->data : nullptr;
-  int64_t ldx = x != nullptr ? x->ld : 0;
+  MlpTensors t{x != nullptr ? x->data : nullptr, w_gate_up, w_down, dy->data,
+               x != nullptr ? x->ld : 0, dy->ld, at<void>(ws, L.h), at<void>(ws, L.dgu)};
   if (dw_gate_up != nullptr && eight_bits(x->format)) {  // exact in bf16: operands as they were kept
     const moe_act_t wide{at<void>(ws, L.x16), nullptr, L.ld_x, cfg->format};
     if ((st = act8_call(T, cfg->hidden, &wide, x, false, stream)) != MOE_OK) return st;
-    x16 = wide.data;
-    ldx = L.ld_x;
+    t.x = wide.data;
+    t.ld_x = L.ld_x;
   }
   TgParams p = mlp_params(cfg, kTgGluBwd, gu, ws);
-  p.dgu = dgu;
+  p.dgu = t.dgu;
   p.ld_dgu = L.ld_dgu;
-  const Product dh{T, D, H, {dy->data, dy->ld, false}, {w_down, D, true},
-                   dw_down != nullptr ? h : nullptr, L.ld_h, 0, 0};
+  const Product dh = dh_product(cfg, T, L, t, dw_down != nullptr);
   if ((st = run_products(&dh, 1, p, s, false)) != MOE_OK) return st;
   Product out[3];
   int n = 0;
   if (dx != nullptr) {
-    out[n++] = Product{T, H, 2 * D, {dgu, L.ld_dgu, false}, {w_gate_up, H, true},
-                       dx->data, dx->ld, 0, 0};
-    if (plan_products(out, 1, kTgStore).small) {  // a launch of its own, whose K loop is split
+    out[n++] = dx_product(cfg, T, L, t, dx->data, dx->ld);
+    if (dx_alone(out[0])) {
       if ((st = run_products(out, 1, mlp_params(cfg, kTgStore, nullptr, ws), s, true)) != MOE_OK)
         return st;
       n = 0;
     }
   }
-  if (dw_gate_up != nullptr)
-    out[n++] = Product{2 * D, H, T, {dgu, L.ld_dgu, true}, {x16, ldx, true}, dw_gate_up, H, f32, acc};
-  if (dw_down != nullptr)
-    out[n++] = Product{H, D, T, {dy->data, dy->ld, true}, {h, L.ld_h, true}, dw_down, D, f32, acc};
+  if (dw_gate_up != nullptr) out[n++] = dw_gate_up_product(cfg, T, L, t, dw_gate_up, f32, acc);
+  if (dw_down != nullptr) out[n++] = dw_down_product(cfg, T, L, t, dw_down, f32, acc);
   if (n == 0) return MOE_OK;
   return run_products(out, n, mlp_params(cfg, kTgStore, nullptr, ws), s, true);
+}
+
+// Not part of the interface: how the launches of a call with contiguous 16-bit activations are
+// tiled, for the tests that cover every form.  forms: gate_up, down, dh, dx (-1: with the weight
+// gradients), the weight gradients (with dx: when it is); a form is a TgShape, or 10 + the CTAs
+// that share a tile of few tokens.  Returns 0 if cfg or T is invalid.
+int32_t moe_mlp_tilings(const moe_mlp_config_t* cfg, int32_t T, int32_t with_dx, int32_t* forms) {
+  if (check_mlp(cfg, T) != MOE_OK || T == 0) return 0;
+  const MlpLayout L = mlp_layout(cfg, T);
+  const MlpTensors t{nullptr, nullptr, nullptr, nullptr, cfg->hidden, cfg->hidden, nullptr, nullptr};
+  auto form = [](const Product* pr, int n, int kind) {
+    const Plan p = plan_products(pr, n, kind);
+    return p.small ? 10 + p.splits : static_cast<int32_t>(p.shape);
+  };
+  const Product up = up_product(cfg, T, L, t), down = down_product(cfg, T, L, t, nullptr, cfg->hidden);
+  const Product dh = dh_product(cfg, T, L, t, true);
+  Product out[3] = {dx_product(cfg, T, L, t, nullptr, cfg->hidden),
+                    dw_gate_up_product(cfg, T, L, t, nullptr, 0, 0),
+                    dw_down_product(cfg, T, L, t, nullptr, 0, 0)};
+  const bool alone = !with_dx || dx_alone(out[0]);
+  forms[0] = form(&up, 1, kTgGluFwd);
+  forms[1] = form(&down, 1, kTgStore);
+  forms[2] = form(&dh, 1, kTgGluBwd);
+  forms[3] = with_dx && alone ? form(out, 1, kTgStore) : -1;
+  forms[4] = alone ? form(out + 1, 2, kTgStore) : form(out, 3, kTgStore);
+  return 1;
 }
 
 }  // extern "C"
