@@ -21,7 +21,9 @@ checkpoints of activations that the backward passes read in place of the activat
 As in the package's other functions, every call checks and marshals its tensors and enqueues
 the library's kernels on a stream (the tensors' device's current one by default).
 Activations are 2-D tensors whose rows are contiguous and may lie further apart than their
-length.  The header states formulas, layouts, limits and errors.
+length.  Nothing is recorded for autograd: outputs that require a gradient are refused outside
+torch.no_grad(), and a written tensor's version goes up, so that a backward pass that had saved
+it raises.  The header states formulas, layouts, limits and errors.
 """
 from __future__ import annotations
 
@@ -197,6 +199,22 @@ def _plain(t, name):
     return t
 
 
+_recording = torch.is_grad_enabled
+# Tells autograd that tensors were written, so that a backward pass that had saved one raises
+# and does not use the new values (torch.autograd.graph.increment_version, without its checks).
+_written = torch._C._increment_version
+
+
+def _no_grad(*outputs):
+    """Nothing here is recorded for autograd, so an output that requires a gradient is refused
+    while autograd records, as torch refuses it as an `out` argument."""
+    if _recording():
+        for t in outputs:
+            if getattr(t, "requires_grad", False):
+                raise ValueError("an output requires a gradient, and these calls record none: "
+                                 "pass a detached tensor or call under torch.no_grad()")
+
+
 def _run(name, index, stream, *args):
     if index < 0:
         raise ValueError(f"{name}: the tensors must be on a CUDA device")
@@ -230,14 +248,17 @@ def moe_act_encode(x, kept: Act8, stream=None) -> None:
     i, rows, cols = _first(_plain(x, "x"), "x")
     _run("moe_act_encode", i, stream, rows, _i32(cols), _act(x, "x", i, rows, cols, None),
          _act(_checkpoint(kept), "kept", i, rows, cols, None))
+    _written((kept.codes, kept.scales))
 
 
 def moe_act_decode(kept: Act8, out, stream=None) -> None:
     """Read an 8-bit checkpoint back into out [rows][cols] (bf16, fp16 or fp32)."""
     i, rows, cols = _first(_plain(out, "out"), "out")
+    _no_grad(out)
     _run("moe_act_decode", i, stream, rows, _i32(cols),
          _act(_checkpoint(kept), "kept", i, rows, cols, None),
          _act(out, "out", i, rows, cols, None))
+    _written((out,))
 
 
 # ------------------------------------------------------------------ norms
@@ -271,12 +292,16 @@ def moe_norm_forward(cfg, x, gain, bias, y, mean, rstd, kept: Act8 | None = None
     norm only), and on request the 8-bit checkpoint of x.  gain and bias may be None."""
     i, T, _ = _first(_plain(x, "x"), "x")
     n, dt, pt, f32 = cfg.cols, cfg.dtype, cfg.param_dtype, torch.float32
+    _no_grad(y, mean, rstd)
     _run("moe_norm_forward", i, stream, cfg._c, _i32(T), _act(x, "x", i, T, n, dt),
          None if gain is None else _ptr(gain, "gain", i, pt, n),
          None if bias is None else _ptr(bias, "bias", i, pt, n),
          _act(_plain(y, "y"), "y", i, T, n, dt),
          None if mean is None else _ptr(mean, "mean", i, f32, T), _ptr(rstd, "rstd", i, f32, T),
          None if kept is None else _act(_checkpoint(kept), "kept", i, T, n, None))
+    _written((y, rstd) if mean is None else (y, mean, rstd))
+    if kept is not None:
+        _written((kept.codes, kept.scales))
 
 
 def moe_norm_backward(cfg, x, gain, mean, rstd, dy, dx, d_gain, d_bias, ws,
@@ -285,6 +310,7 @@ def moe_norm_backward(cfg, x, gain, mean, rstd, dy, dx, d_gain, d_bias, ws,
     checkpoint and the forward pass's statistics.  accumulate adds to d_gain and d_bias."""
     i, T, _ = _first(x, "x")
     n, dt, f32 = cfg.cols, cfg.dtype, torch.float32
+    _no_grad(dx, d_gain, d_bias)
     _run("moe_norm_backward", i, stream, cfg._c, _i32(T), _act(x, "x", i, T, n, dt),
          None if gain is None else _ptr(gain, "gain", i, cfg.param_dtype, n),
          None if mean is None else _ptr(mean, "mean", i, f32, T), _ptr(rstd, "rstd", i, f32, T),
@@ -292,6 +318,7 @@ def moe_norm_backward(cfg, x, gain, mean, rstd, dy, dx, d_gain, d_bias, ws,
          None if d_gain is None else _ptr(d_gain, "d_gain", i, f32, n),
          None if d_bias is None else _ptr(d_bias, "d_bias", i, f32, n), 1 if accumulate else 0,
          _ptr(ws, "ws", i, torch.uint8, None), ws.numel())
+    _written([t for t in (dx, d_gain, d_bias) if t is not None])
 
 
 # ------------------------------------------------------------------ the gated MLP
@@ -322,11 +349,14 @@ def moe_mlp_forward(cfg, x, w_gate_up, w_down, y, ws, kept_gu=None, stream=None)
     it, a [T][2D] tensor or an Act8 of two parts."""
     i, T, _ = _first(_plain(x, "x"), "x")
     H, D, dt = cfg.hidden, cfg.inter, cfg.dtype
+    _no_grad(y, kept_gu)
     _run("moe_mlp_forward", i, stream, cfg._c, _i32(T), _act(x, "x", i, T, H, dt),
          _ptr(w_gate_up, "w_gate_up", i, dt, 2 * D * H), _ptr(w_down, "w_down", i, dt, D * H),
          _act(_plain(y, "y"), "y", i, T, H, dt),
          None if kept_gu is None else _act(kept_gu, "kept_gu", i, T, D, dt, 2),
          _ptr(ws, "ws", i, torch.uint8, None), ws.numel())
+    _written((y,) if kept_gu is None else (y, kept_gu.codes, kept_gu.scales)
+             if isinstance(kept_gu, Act8) else (y, kept_gu))
 
 
 def moe_mlp_backward(cfg, x, gu, w_gate_up, w_down, dy, dx, dw_gate_up, dw_down, ws,
@@ -339,6 +369,7 @@ def moe_mlp_backward(cfg, x, gu, w_gate_up, w_down, dy, dx, dw_gate_up, dw_down,
     grad = next((g.dtype for g in (dw_gate_up, dw_down) if g is not None), dt)
     if grad not in (dt, torch.float32):
         raise TypeError(f"weight gradients must be {dt} or torch.float32, got {grad}")
+    _no_grad(dx, dw_gate_up, dw_down)
     _run("moe_mlp_backward", i, stream, cfg._c, _i32(T),
          None if x is None and dw_gate_up is None else _act(x, "x", i, T, H, dt),
          _act(gu, "gu", i, T, D, dt, 2),
@@ -349,3 +380,4 @@ def moe_mlp_backward(cfg, x, gu, w_gate_up, w_down, dy, dx, dw_gate_up, dw_down,
          None if dw_gate_up is None else _ptr(dw_gate_up, "dw_gate_up", i, grad, 2 * D * H),
          None if dw_down is None else _ptr(dw_down, "dw_down", i, grad, D * H), _FORMATS[grad],
          1 if accumulate else 0, _ptr(ws, "ws", i, torch.uint8, None), ws.numel())
+    _written([t for t in (dx, dw_gate_up, dw_down) if t is not None])
