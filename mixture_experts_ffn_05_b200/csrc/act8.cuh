@@ -29,7 +29,7 @@ __device__ __forceinline__ int scale_byte(uint32_t amax_bits) {
   return amax_bits >= 0x7F800000u ? kBadScale : b;
 }
 
-// 2^k and 2^-k of a scale byte (k + 127 in 1..248, so both are normal); NaN of a bad one.
+// 2^k and 2^-k of a scale byte (k + 127 in 1..249, so both are normal); NaN of a bad one.
 __device__ __forceinline__ float scale_value(int byte) {
   return byte == kBadScale ? __uint_as_float(0x7FC00000u)
                            : __uint_as_float(static_cast<uint32_t>(byte) << 23);

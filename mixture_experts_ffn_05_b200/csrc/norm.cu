@@ -9,9 +9,10 @@
 // 50 to 200 KB of loads in flight per SM without registers and whatever phase the teams are
 // in.  Gain and bias lie in shared memory in fp32.
 //
-// What is left to the instruction slots decides beside HBM: a row costs a warp about 9 NV + 8
-// tens of instructions (the sums over lanes and warps, the ring, the row's addresses), so NV is
-// what makes W (8 NV + 9) smallest: 2816 columns take 4 warps of 24 elements.
+// Beside HBM a row's instructions and the latency of its sums decide (2.3 to 2.6 instructions a
+// cycle of 4 at 16384 x 2816): a row costs a warp about 8 NV + 9 tens of instructions (the sums
+// over lanes and warps, the ring, the row's addresses), so NV is what makes W (8 NV + 9)
+// smallest: 2816 columns take 4 warps of 24 elements.
 //
 // Wide form (columns, strides and bases that 16-byte accesses fit): a thread owns units of 16
 // bytes of the activation's format, U = 8 or 4 columns; it reads back only the units that it
@@ -35,9 +36,12 @@ constexpr int kNormSmem = 226 * 1024;         // of a CTA
 constexpr int kNormMaxStages = 4;
 constexpr int kNormRed = 2 * 768 / 32;         // floats of a round of sums: two a warp
 
-// Threads of a CTA: as many as the registers of 8 NV elements allow without spills (which, the
-// ring leaving little of L1, would go to L2).  NV = 4 only serves rows of more than 12288
-// columns (layer norm's backward: 9216), and spills in backward.
+// Threads of a CTA: as many as the registers of 8 NV elements allow with next to no spills
+// (which, the ring leaving little of L1, would go to L2): 20 bytes at most up to NV = 3 (narrow
+// layer norm forward at NV = 2, fp32 RMS backward at NV = 3).  NV = 4 only serves rows of more
+// than 12288 columns (layer norm's backward: 9216) and spills in backward, 16 to 130 bytes for
+// RMS and 350 to 390 for layer norm: 4096 x 16384 in bf16 takes 122 and 185 us there, 62 at the
+// copy's rate, and layer norm's 4096 x 12288 161 us where 9216 columns at NV = 3 take 68.
 __host__ __device__ constexpr int norm_forward_threads(int nv) {
   return nv <= 2 ? 768 : nv == 3 ? 640 : 512;
 }

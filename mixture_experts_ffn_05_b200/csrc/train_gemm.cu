@@ -294,6 +294,7 @@ __device__ __forceinline__ void read_kept(const TgParams& P, uint4* stage, const
   }
 }
 
+// The epilogues hold 32 columns of up to three matrices; that of dh spills 12 bytes a thread.
 // h = act(g) u, over g.
 template <bool SILU>
 __device__ __forceinline__ void glu_forward(float (&g)[32], const float (&u)[32]) {
