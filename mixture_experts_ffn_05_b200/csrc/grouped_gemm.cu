@@ -226,10 +226,14 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, int mode) {
   return static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
 }
 
-template <int BN, bool W8, bool PAIR>
+// TOK: the launches of a call whose gate_up has P.token_rows (a variant of its own: the
+// producer's loop is slower with the choice in it, T = 8 and 64 by 0.6%; the down launch of such a
+// call takes it too, since a second kernel's code cost 0.6 to 1 us more).
+template <int BN, bool W8, bool PAIR, bool TOK>
 __global__ void __launch_bounds__((Cfg<BN, W8, PAIR>::kThreads), 1)
     grouped_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmParams P) {
   using C = Cfg<BN, W8, PAIR>;
+  static_assert(!TOK || C::kTok > 0, "token rows come with the narrowest tiles");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__((Cfg<BN, W8, PAIR>::kThreads), 1)
   // its own results, and the producer loads them after the dependency wait.  Where that
   // kernel wrote the tables as well (token_rows), everything from here on waits for it; the
   // next launch reads them early, so it may start only then.
-  const bool by_token = C::kTok > 0 && P.token_rows != nullptr;
+  const bool by_token = TOK && P.token_rows != nullptr;
   if (by_token) pdl_wait();
   pdl_trigger();
   if (by_token && static_cast<int>(threadIdx.x) < min(C::kTok, P.prob[0].n_tokens))
@@ -1047,11 +1051,11 @@ __global__ void __launch_bounds__((Cfg<BN, W8, PAIR>::kThreads), 1)
   }
 }
 
-template <int BN, bool W8, bool PAIR>
+template <int BN, bool W8, bool PAIR, bool TOK = false>
 static cudaError_t launch_bn(const GemmMaps& maps, const GemmParams& p, int grid, cudaStream_t s,
                              bool pdl) {
   using C = Cfg<BN, W8, PAIR>;
-  auto kernel = grouped_gemm_kernel<BN, W8, PAIR>;
+  auto kernel = grouped_gemm_kernel<BN, W8, PAIR, TOK>;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
@@ -1094,6 +1098,11 @@ cudaError_t launch_grouped_gemm(int bn, const GemmMaps& maps, const GemmParams& 
   // split K only with BN = 16 (wider tiles split their epilogue by columns instead)
   for (int i = 0; i < p.nprob; ++i)
     if (bn != 16 && p.prob[i].split > 1) return cudaErrorInvalidValue;
+  if (p.direct) {
+    if (bn != 16 || p.pairs || p.int8_weights || p.prob[0].n_tokens > kTokenRows)
+      return cudaErrorInvalidValue;
+    return launch_bn<16, false, false, true>(maps, p, grid, s, pdl);
+  }
   if (p.pairs) {
     if (!gemm_pairs_allowed(bn, p.int8_weights != 0)) return cudaErrorInvalidValue;
 

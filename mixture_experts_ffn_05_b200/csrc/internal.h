@@ -59,6 +59,7 @@ struct GemmParams {
   // wrote these rows and the offsets.  NULL: the B operand's rows lie in sorted order.
   const int* token_rows;
   int top_k;
+  int direct;           // both launches of a call whose gate_up has token_rows
   float* partials;      // split-K partial tiles, [piece][BN][128] fp32
   unsigned* counters;   // split-K arrival counters, zero between launches
   unsigned* sched;      // [2] piece counter and finished CTAs (single-CTA launches), zero

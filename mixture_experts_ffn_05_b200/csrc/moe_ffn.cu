@@ -503,6 +503,7 @@ moe_status_t run_gemms(const Dims& d, const Layout& L, void* ws, const GemmJob& 
   const bool w8 = j.experts && d.int8;
   gu.token_rows = j.direct ? j.sorted_src : nullptr;
   gu.top_k = d.k;
+  gu.direct = dn.direct = j.direct ? 1 : 0;
   gu.sched = at<unsigned>(ws, L.sched);
   dn.sched = at<unsigned>(ws, L.sched) + 2;  // the down launch may start before gate_up ends
   for (GemmParams* P : {&gu, &dn}) {
