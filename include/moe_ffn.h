@@ -31,9 +31,9 @@
  *     be at least moe_workspace_size(cfg, T) and 256-byte aligned.  A new workspace
  *     must be zeroed once before its first use (e.g. cudaMemsetAsync); every call that
  *     completes leaves its counters at zero again, so later calls need no clearing.
- *     It serves calls of any T and cfg that it is large enough for, in any order.  The
- *     size is not monotonic in T (the smallest batches split K): for batches of several
- *     sizes take the largest of their sizes.
+ *     It serves calls of any T and cfg that it is large enough for, in any order, those
+ *     of moe_train.h too.  The size is not monotonic in T (the smallest batches split K):
+ *     for batches of several sizes take the largest of their sizes.
  *     After MOE_ERR_DEVICE_TIMEOUT, zero the workspace again.  A workspace that was
  *     not zeroed gives wrong results, never an out-of-bounds access or a hang.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).  Every call

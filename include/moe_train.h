@@ -15,9 +15,9 @@
  *   - 0 <= T <= 2^31 - 512 rows.  T = 0 computes nothing, but weight gradients that are not
  *     accumulated are set to zero.
  *   - A workspace is 256-byte aligned and zeroed once before its first use; its first word
- *     is the status word that moe_check_device_status() reads.  Calls whose kernels may
- *     overlap on the GPU (other streams, other captured graphs) need workspaces of their
- *     own.
+ *     is the status word that moe_check_device_status() reads.  It serves any calls in turn
+ *     that it is large enough for, those of moe_ffn.h too.  Calls whose kernels may overlap
+ *     on the GPU (other streams, other captured graphs) need workspaces of their own.
  */
 #ifndef MOE_TRAIN_H
 #define MOE_TRAIN_H

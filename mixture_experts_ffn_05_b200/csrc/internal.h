@@ -13,6 +13,21 @@ namespace moe {
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 int device_sm_count();
 
+// The start of every workspace: the words that must be zero between calls, at the same place for
+// every batch size, configuration and entry point, so that no call finds another one's data in
+// them.  The status word; the last-CTA chains of the routers (one word a token block or tile: at
+// most 17 of the small-batch router's, 74 of the tensor-core router's, which has several slices
+// up to there); the piece counters of the two GEMM launches; and one word per split tile.
+// Launches split K when they have few tiles (choose_split: 8 * 148 expected, which bounds the
+// pieces by about 23500; stream_splits: a few pieces a CTA); one with more tiles than words does
+// not split.  Every call's data lies behind kWsData.
+constexpr int kRouterWords = 256;
+constexpr int kCounterWords = 65536;
+constexpr size_t kWsRouterWords = 256;
+constexpr size_t kWsSched = kWsRouterWords + kRouterWords * 4;
+constexpr size_t kWsCounters = kWsSched + 256;
+constexpr size_t kWsData = (kWsCounters + kCounterWords * 4 + 1023) / 1024 * 1024;
+
 // One GEMM problem of a grouped launch.  The weights are the M operand (rows of a
 // K-major matrix streamed by TMA), the tokens the N operand.  Output row = B row.
 //   kind 0 (gate_up): each M tile holds 64 features of one group as 8 gate rows, the

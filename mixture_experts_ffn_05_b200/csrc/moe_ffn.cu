@@ -121,16 +121,6 @@ bool rows_direct(const Dims& d) {
 // of the launch (five CTAs per SM assumed), at least 32 KB and four K items each.
 constexpr int kStreamAssumedCtas = 5 * kAssumedSms;
 
-// Words of a workspace that must be zero between calls, at the same place for every batch
-// size and configuration, so that no call finds another one's data in them: the last-CTA
-// chains of the routers (one word a token block or tile: at most 17 of the small-batch
-// router's, 74 of the tensor-core router's, which has several slices up to there), the piece
-// counters of the two GEMM launches, and one word per split tile.  Launches split K when they
-// have few tiles (choose_split: 8 * 148 expected, which bounds the pieces by about 23500;
-// stream_splits: a few pieces a CTA); one with more tiles than words does not split.
-constexpr int kRouterWords = 256;
-constexpr int kCounterWords = 65536;
-
 struct StreamSplits {
   int gu_e, gu_d, dn_e, dn_d;  // K pieces: gate_up experts / dense, down experts / dense
   int nt_e, nt_d;              // token n-tiles of 8 per unit: experts / dense (both launches)
@@ -238,10 +228,10 @@ Layout layout_of(const Dims& d) {
     return at;
   };
   L.status = 0;
-  L.rcounters = 256;
-  L.sched = L.rcounters + kRouterWords * 4;  // [0..1] gate_up, [2..3] down
-  L.counters = L.sched + 256;
-  off = align_up(L.counters + kCounterWords * 4, kAlign);
+  L.rcounters = kWsRouterWords;
+  L.sched = kWsSched;  // [0..1] gate_up, [2..3] down
+  L.counters = kWsCounters;
+  off = kWsData;
   L.logits = take(static_cast<size_t>(T) * d.E * 4);
   L.bhist = take(static_cast<size_t>(nb) * d.E * 4);
   L.bbase = take(static_cast<size_t>(nb) * d.E * 4);

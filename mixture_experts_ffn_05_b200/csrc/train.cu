@@ -94,7 +94,7 @@ moe_status_t check_mlp(const moe_mlp_config_t* c, int32_t T) {
 }
 
 struct MlpLayout {
-  size_t h, dgu, x16, total;  // after the status word
+  size_t h, dgu, x16, total;
   int64_t ld_h, ld_dgu, ld_x; // rows start on 128-byte lines, as the copies like them best
 };
 
@@ -104,7 +104,7 @@ MlpLayout mlp_layout(const moe_mlp_config_t* c, int32_t T) {
   L.ld_h = static_cast<int64_t>((D + 63) / 64 * 64);
   L.ld_dgu = static_cast<int64_t>((2 * D + 63) / 64 * 64);
   L.ld_x = static_cast<int64_t>((H + 63) / 64 * 64);
-  L.h = kAlign;
+  L.h = kWsData;
   L.dgu = L.h + align_up(t * L.ld_h * 2);
   L.x16 = L.dgu + align_up(t * L.ld_dgu * 2);
   L.total = L.x16 + align_up(t * L.ld_x * 2);
@@ -366,7 +366,7 @@ moe_status_t moe_norm_forward(const moe_norm_config_t* cfg, int32_t T, const moe
 size_t moe_norm_workspace_size(const moe_norm_config_t* cfg, int32_t T) {
   if (check_norm(cfg, T) != MOE_OK) return 0;
   const size_t rows = norm_backward_max_ctas(T);
-  return kAlign + align_up(rows * 2 * cfg->cols * sizeof(float));
+  return kWsData + align_up(rows * 2 * cfg->cols * sizeof(float));
 }
 
 moe_status_t moe_norm_backward(const moe_norm_config_t* cfg, int32_t T, const moe_act_t* x,
@@ -405,7 +405,7 @@ moe_status_t moe_norm_backward(const moe_norm_config_t* cfg, int32_t T, const mo
   a.d_gain = d_gain;
   a.d_bias = d_bias;
   a.accumulate = accumulate != 0;
-  a.partials = at<float>(ws, kAlign);
+  a.partials = at<float>(ws, kWsData);
   return cuda_status(launch_norm_backward(a, cfg->format, x->format, s));
 }
 

@@ -5,6 +5,7 @@ import torch
 
 import mixture_experts_ffn_05_b200 as mf
 import synth
+from mixture_experts_ffn_05_b200 import train
 from tests import cases
 from tests.gpu_util import (config, device_layer, fp8_experts, int8_experts, nvfp4_experts, to_dev)
 
@@ -100,3 +101,33 @@ def test_stack_whose_last_chunk_is_short(rest):
         mf.moe_stack_forward(cfg, x, layers, out, ws, chunk_tokens=1024)
         assert mf.moe_check_device_status(ws) == mf.MOE_OK
         assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+def test_blocks_and_training_calls_in_turn():
+    """Inference of a block and training passes of its dense branch on one workspace."""
+    from tests.test_gpu_train_mlp import Case as MlpCase
+    from tests.test_gpu_train_norm import Case as NormCase
+
+    c = cases.make_case(SMALL, seed=48, gap=False)
+    cfg = config(SMALL)
+    bw = mf.BlockWeights(cfg, device_layer(c))
+    x = to_dev(synth.x_rows(49, SMALL.H, 300))
+    sizes = (8, 300, 3, 64)
+    mcfg, ncfg = train.MlpConfig(SMALL.H, SMALL.D), train.NormConfig(SMALL.H, "layer")
+    need = max(max(mf.workspace_size(cfg, T), train.mlp_workspace(mcfg, T).numel(),
+                   train.norm_workspace(ncfg, T).numel()) for T in sizes)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for T in sizes:
+        want = block(cfg, bw, x[:T], mf.workspace(cfg, T))
+        m = MlpCase(T, SMALL.H, SMALL.D, keep="int8", seed=T).forward().backward()
+        n = NormCase(T, SMALL.H, "layer", seed=T).run()
+        outs = (m.y, m.dx, m.dwgu, m.dwd, n.y, n.dx, n.d_gain, n.d_bias)
+        first = [t.clone() for t in outs]
+        m.ws = n.ws = ws
+        for _ in range(2):
+            m.forward().backward()
+            n.run()
+            for a, b in zip(outs, first):
+                assert torch.equal(a, b)
+            for a, b in zip(block(cfg, bw, x[:T], ws), want):
+                assert torch.equal(a.view(torch.int16), b.view(torch.int16))
