@@ -425,7 +425,8 @@ __global__ void __launch_bounds__((Cfg<BN, W8, PAIR>::kThreads), 1)
       };
       int n_pushed = 0;
       int piece = C::kDyn ? static_cast<int>(atomicAdd(P.sched, 1u)) : first_item;
-      for (; piece < total && ok;) {
+      // (a counter that does not start at zero gives a wrong result, never a piece that is none)
+      for (; piece >= 0 && piece < total && ok;) {
         // the next piece is taken one ahead, so the atomic's latency hides behind loads
         const int next = C::kDyn ? static_cast<int>(atomicAdd(P.sched, 1u)) : piece + item_stride;
         if (C::kDyn && !q_push(n_pushed++, piece)) {

@@ -131,3 +131,23 @@ def test_blocks_and_training_calls_in_turn():
                 assert torch.equal(a, b)
             for a, b in zip(block(cfg, bw, x[:T], ws), want):
                 assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("start", [-16, -1000000, 5])
+def test_a_piece_counter_that_is_not_zero(start):
+    """A workspace that was not zeroed gives wrong results at most: pieces below zero or past the
+    end are nobody's."""
+    c = cases.make_case(SMALL, seed=50, gap=False)
+    cfg = config(SMALL)
+    bw = mf.BlockWeights(cfg, device_layer(c))
+    T = 100  # tiles of 64 tokens, whose pieces come from the counter
+    x = to_dev(synth.x_rows(51, SMALL.H, T))
+    ws = mf.workspace(cfg, T)
+    want = block(cfg, bw, x, ws)
+    ws[256 + 1024:256 + 1024 + 12].view(torch.int32)[[0, 2]] = start
+    out = torch.empty_like(x)
+    mf.moe_block_forward(cfg, x, bw, out, ws)
+    torch.cuda.synchronize()
+    ws.zero_()
+    for a, b in zip(block(cfg, bw, x, ws), want):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
