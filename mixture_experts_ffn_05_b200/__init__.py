@@ -157,7 +157,15 @@ def _ptr(t, dtype=None, name="tensor", nullable=False):
     return t.data_ptr()
 
 
-def _stream(stream):
+_current_device = torch._C._cuda_getDevice
+
+
+def _stream(stream, t):
+    """The stream's handle.  t: a tensor of the call, which must be on the current device, where
+    the call's kernels run."""
+    if t.get_device() != _current_device():
+        raise ValueError(f"the call's tensors are on {t.device}, the current device is "
+                         f"cuda:{_current_device()}: call under torch.cuda.device({t.device!r})")
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
 
@@ -188,7 +196,7 @@ def moe_router(cfg, x, router_scale, w_router, logit_bias, per_expert_scale, g_p
                           _ptr(g_pre_moe, BF16, "g_pre_moe"), _ptr(g_pre_dense, BF16, "g_pre_dense"),
                           _ptr(topk_idx, torch.int32, "topk_idx"), _ptr(topk_w, torch.float32, "topk_w"),
                           _ptr(xn_moe, BF16, "xn_moe"), _ptr(xn_dense, BF16, "xn_dense"),
-                          _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+                          _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream, x))
     _check("moe_router", st)
 
 
@@ -198,7 +206,7 @@ def moe_permute(cfg, topk_idx, expert_offsets, sorted_src, inv_pos, ws, stream=N
                            _ptr(expert_offsets, torch.int32, "expert_offsets"),
                            _ptr(sorted_src, torch.int32, "sorted_src"),
                            _ptr(inv_pos, torch.int32, "inv_pos"), _ptr(ws, torch.uint8, "ws"),
-                           ws.numel(), _stream(stream))
+                           ws.numel(), _stream(stream, topk_idx))
     _check("moe_permute", st)
 
 
@@ -210,7 +218,7 @@ def moe_permute_noalloc(cfg, topk_idx, expert_offsets, sorted_src, inv_pos, stre
     st = lib().moe_permute_noalloc(ctypes.byref(cfg.c()), T, _ptr(topk_idx, torch.int32, "topk_idx"),
                                    _ptr(expert_offsets, torch.int32, "expert_offsets"),
                                    _ptr(sorted_src, torch.int32, "sorted_src"),
-                                   _ptr(inv_pos, torch.int32, "inv_pos"), _stream(stream))
+                                   _ptr(inv_pos, torch.int32, "inv_pos"), _stream(stream, topk_idx))
     _check("moe_permute_noalloc", st)
 
 
@@ -233,7 +241,7 @@ def moe_ffn_forward(cfg, xn_moe, topk_w, expert_offsets, sorted_src, inv_pos, ex
                                _ptr(sorted_src, torch.int32, "sorted_src"),
                                _ptr(inv_pos, torch.int32, "inv_pos"), ctypes.byref(ew),
                                _ptr(moe_out, BF16, "moe_out"), _ptr(ws, torch.uint8, "ws"),
-                               ws.numel(), _stream(stream))
+                               ws.numel(), _stream(stream, xn_moe))
     _check("moe_ffn_forward", st)
 
 
@@ -242,7 +250,7 @@ def dense_mlp_forward(cfg, xn_dense, w_gate_up, w_down, dense_out, ws, stream=No
     st = lib().dense_mlp_forward(ctypes.byref(cfg.c()), T, _ptr(xn_dense, BF16, "xn_dense"),
                                  _ptr(w_gate_up, BF16, "w_gate_up"), _ptr(w_down, BF16, "w_down"),
                                  _ptr(dense_out, BF16, "dense_out"), _ptr(ws, torch.uint8, "ws"),
-                                 ws.numel(), _stream(stream))
+                                 ws.numel(), _stream(stream, xn_dense))
     _check("dense_mlp_forward", st)
 
 
@@ -287,7 +295,7 @@ def moe_block_forward(cfg, x, weights: BlockWeights, out, ws, moe_out=None, stre
     st = lib().moe_block_forward(ctypes.byref(cfg.c()), T, _ptr(x, BF16, "x"),
                                  ctypes.byref(weights.c), _ptr(out, BF16, "out"),
                                  _ptr(moe_out, BF16, "moe_out", True), _ptr(ws, torch.uint8, "ws"),
-                                 ws.numel(), _stream(stream), ev)
+                                 ws.numel(), _stream(stream, x), ev)
     _check("moe_block_forward", st)
 
 
@@ -310,7 +318,7 @@ def moe_stack_forward(cfg, x, layers, out, ws, chunk_tokens: int = 16384, stream
     arr = (CBlockWeights * len(layers))(*[l.c for l in layers])
     st = lib().moe_stack_forward(ctypes.byref(cfg.c()), T, _ptr(x, BF16, "x"), arr, len(layers),
                                  _ptr(out, BF16, "out"), int(chunk_tokens),
-                                 _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+                                 _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream, x))
     _check("moe_stack_forward", st)
 
 
@@ -318,7 +326,7 @@ def moe_quantize_int8(w, q, scales, stream=None):
     cols = w.shape[-1]
     rows = w.numel() // cols
     st = lib().moe_quantize_int8(_ptr(w, BF16, "w"), rows, cols, _ptr(q, torch.int8, "q"),
-                                 _ptr(scales, torch.float32, "scales"), _stream(stream))
+                                 _ptr(scales, torch.float32, "scales"), _stream(stream, w))
     _check("moe_quantize_int8", st)
 
 
@@ -327,7 +335,7 @@ def moe_quantize_fp8(w, q, scales, stream=None):
     cols = w.shape[-1]
     rows = w.numel() // cols
     st = lib().moe_quantize_fp8(_ptr(w, BF16, "w"), rows, cols, _ptr(q, torch.uint8, "q"),
-                                _ptr(scales, torch.float32, "scales"), _stream(stream))
+                                _ptr(scales, torch.float32, "scales"), _stream(stream, w))
     _check("moe_quantize_fp8", st)
 
 
@@ -342,7 +350,7 @@ def moe_quantize_nvfp4(w, q, block_scales, tensor_scales, stream=None):
                                   _ptr(q, torch.uint8, "q"),
                                   _ptr(block_scales, torch.uint8, "block_scales"),
                                   _ptr(tensor_scales, torch.float32, "tensor_scales"),
-                                  _stream(stream))
+                                  _stream(stream, w))
     _check("moe_quantize_nvfp4", st)
 
 
@@ -350,7 +358,7 @@ def moe_wait_selftest(ws, timeout_ns: int, stream=None) -> None:
     """Run one bounded device wait that is bound to run out (the failure path of every
     kernel's waits); afterwards moe_check_device_status reports MOE_ERR_DEVICE_TIMEOUT."""
     _check("moe_wait_selftest", lib().moe_wait_selftest(_ptr(ws, torch.uint8, "ws"), ws.numel(),
-                                                         int(timeout_ns), _stream(stream)))
+                                                         int(timeout_ns), _stream(stream, ws)))
 
 
 def moe_block_launch_count(cfg, T: int) -> int:
@@ -359,6 +367,8 @@ def moe_block_launch_count(cfg, T: int) -> int:
 
 
 def moe_check_device_status(ws, stream=None) -> int:
-    """Waits for the stream; returns the status recorded by the last call's kernels."""
-    return int(lib().moe_check_device_status(_ptr(ws, torch.uint8, "ws"), ws.numel(),
-                                             _stream(stream)))
+    """Waits for the stream (by default the current one of ws's device); returns the status
+    recorded by the last call's kernels."""
+    p = _ptr(ws, torch.uint8, "ws")
+    with torch.cuda.device(ws.get_device()):
+        return int(lib().moe_check_device_status(p, ws.numel(), _stream(stream, ws)))
