@@ -107,7 +107,7 @@ bool stream_path(const Dims& d) { return d.nvfp4 || (d.int8 && d.T <= kStreamMax
 // Batches of at most kTokenRows (token, slot) pairs in one token block of the small-batch
 // router have no gather: the gate_up launch loads each routed row of xn_moe where it lies.
 // It waits for the router before it can pick its pieces, where behind a gather it would fill
-// its ring meanwhile, and still takes less time: bf16 T = 1, 2, 4 in 51.2, 65.6, 89.6 us
+// its ring meanwhile, and still takes less time: bf16 T = 1, 2, 4 in 51.2, 65.9, 89.8 us
 // against 52.6, 66.9, 90.4 with the gather as a launch of its own.  The weight-streaming
 // kernel (int8, NVFP4) and the quantised rows of fp8 need the gather.
 constexpr int kDirectMaxTokens = 8;
